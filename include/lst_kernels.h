@@ -100,6 +100,36 @@ lst_status lst_k_attention_bwd(const uint16_t* q, int64_t ldq, const uint16_t* k
                                uint16_t* dv, int64_t lddv, int64_t T, int32_t S, int32_t hq,
                                int32_t hkv, int32_t hd, void* stream);
 
+/* Attention under a sliding window with sinks, forward: key j of a sequence is visible to its query i
+ * when j <= i and (i - j < window or j < sinks); window >= S is plain causal attention. Long answers
+ * are sampled this way, with a cache of the last `window` tokens and the first `sinks` ones; training
+ * on them has to see the same keys. Arguments as lst_k_attention_fwd (any hq a multiple of hkv), o
+ * 16-byte aligned with ldo a multiple of 8; window >= 1, sinks >= 0; T * hq below 2^31. The
+ * probabilities enter the P V product as bf16, so v has bf16's range. Rows of one sequence never
+ * reach another's result; within a sequence a NaN or infinity in k or v may reach queries that share
+ * a 128-row tile with its visible ones. */
+lst_status lst_k_attention_window_fwd(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk,
+                                      const uint16_t* v, int64_t ldv, uint16_t* o, int64_t ldo,
+                                      float* lse, int64_t T, int32_t S, int32_t hq, int32_t hkv,
+                                      int32_t hd, int32_t window, int32_t sinks, void* stream);
+
+/* Its backward: dq, dk, dv bf16 (16-byte aligned, row strides multiples of 8) from dout and the
+ * forward's o and lse; dk and dv add the query heads of their group. scratch: fp32
+ * [lst_k_attention_window_scratch(...)], 16-byte aligned, not shared by calls that may overlap on the
+ * GPU; its first T * hq values come back as rowsum(dout * o). Deterministic (no atomics). */
+lst_status lst_k_attention_window_bwd(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk,
+                                      const uint16_t* v, int64_t ldv, const uint16_t* o, int64_t ldo,
+                                      const uint16_t* dout, int64_t lddo, const float* lse,
+                                      float* scratch, uint16_t* dq, int64_t lddq, uint16_t* dk,
+                                      int64_t lddk, uint16_t* dv, int64_t lddv, int64_t T, int32_t S,
+                                      int32_t hq, int32_t hkv, int32_t hd, int32_t window,
+                                      int32_t sinks, void* stream);
+
+/* fp32 values of scratch of lst_k_attention_window_bwd for these sizes; -1 for sizes that it refuses.
+ * Needs no GPU. */
+int64_t lst_k_attention_window_scratch(int64_t T, int32_t S, int32_t hq, int32_t hkv, int32_t hd,
+                                       int32_t window, int32_t sinks);
+
 /* RMSNorm forward of the fp32 residual stream x [T, d]: y = bf16(x * rstd * g), rstd [T]. */
 lst_status lst_k_rmsnorm_fwd(const float* x, const float* g, int64_t T, int32_t d, float eps,
                              uint16_t* y, float* rstd, void* stream);
@@ -124,6 +154,40 @@ lst_status lst_k_swiglu_bwd(const float* dm, const uint16_t* gu, int64_t T, int3
 /* Cross-entropy rows over fp32 logits [T, V]: loss_rows [T], dlogits bf16 [T, V] scaled by inv_T. */
 lst_status lst_k_cross_entropy(const float* logits, int64_t T, int32_t V, const int32_t* targets,
                                float inv_T, float* loss_rows, uint16_t* dlogits, void* stream);
+
+/* How the terms of the policy loss are weighted (m_t = 1 on counted tokens, else 0): by
+ * m_t / sum m (mean over tokens), m_t / (nseq * sum of m over the token's sequence) (mean over the
+ * sequences of their means; a sequence without a counted token adds 0), m_t / T. */
+enum { LST_POLICY_TOKEN_MEAN = 0, LST_POLICY_SEQ_MEAN = 1, LST_POLICY_FIXED = 2 };
+
+typedef struct {
+  float clip_lo;        /* in [0, 1]: the ratio's lower bound is 1 - clip_lo */
+  float clip_hi;        /* >= 0: its upper bound is 1 + clip_hi; infinity: none */
+  float kl_beta;        /* >= 0, finite: weight of the KL term */
+  int32_t norm;         /* LST_POLICY_* */
+  int32_t adv_per_seq;  /* 1: one advantage a sequence [T / S]; 0: one a token [T] */
+} lst_policy;
+
+/* Clipped policy loss with a KL term and its gradient with respect to the logits, over T tokens in
+ * sequences of S (T a multiple of S). Per counted token (mask[t] != 0; mask NULL: all):
+ *   logp_t = logits[t][y_t] - logsumexp(logits[t]),  r = exp(logp_t - old_logp[t]),
+ *   u = min(r A, clip(r, 1 - clip_lo, 1 + clip_hi) A),
+ *   kl = exp(ref_logp[t] - logp_t) - (ref_logp[t] - logp_t) - 1,  l_t = -u + kl_beta kl;
+ * out [4] = sums of w_t times l_t (the loss), kl, 1 where the clip lowered u else 0, and r;
+ * logp [T] = logp_t (0 on tokens that do not count);
+ * dlogits bf16 [T, V] (NULL: loss only) = w_t dl_t/dlogp_t (onehot(y_t) - softmax(logits[t])), with
+ * no gradient through u where the clip lowered it; 0 on tokens that do not count, whose logits and
+ * targets are not read for values. old_logp NULL: the policy is the one that sampled (r = 1).
+ * ref_logp NULL: no KL term (kl_beta must be 0). A target out of range is reported (device error 2)
+ * and its token adds nothing. V up to 2^20. scratch: fp32 [lst_k_policy_scratch(T, S)], 16-byte
+ * aligned, not shared by calls that may overlap on the GPU. cfg: HOST memory. Deterministic. */
+lst_status lst_k_policy_loss(const float* logits, int64_t T, int32_t V, const int32_t* targets, int32_t S,
+                             const float* old_logp, const float* ref_logp, const float* adv,
+                             const int32_t* mask, const lst_policy* cfg, float* logp, float* out,
+                             uint16_t* dlogits, float* scratch, void* stream);
+
+/* fp32 values of scratch of lst_k_policy_loss; -1 unless T is a positive multiple of S. Needs no GPU. */
+int64_t lst_k_policy_scratch(int64_t T, int32_t S);
 
 /* LoRA skinny projection Us = bf16(s * X Bop) of the side path ("Fine-Tuning an 8B Parameter
  * Model on a 4 GB Laptop GPU", section "LoRA and QLoRA"): X bf16 [T, K] (row stride ldx); Bop bf16

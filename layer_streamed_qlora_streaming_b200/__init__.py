@@ -99,6 +99,13 @@ _SIGS = {
                                    _I32, _I32, _P]),
     "lst_k_attention_bwd": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P,
                                    _I64, _P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _I32, _P]),
+    "lst_k_attention_window_fwd": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I32, _I32, _I32,
+                                          _I32, _I32, _P]),
+    "lst_k_attention_window_bwd": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P,
+                                          _I64, _P, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _P]),
+    "lst_k_attention_window_scratch": (_I64, [_I64, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "lst_k_policy_loss": (_I32, [_P, _I64, _I32, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "lst_k_policy_scratch": (_I64, [_I64, _I32]),
     "lst_k_rmsnorm_fwd": (_I32, [_P, _P, _I64, _I32, _F32, _P, _P, _P]),
     "lst_k_rmsnorm_bwd": (_I32, [_P, _P, _P, _P, _P, _I64, _I32, _P, _P, _P]),
     "lst_k_rope_tables": (_I32, [_I32, _I32, _F64, _P, _P, _P]),
@@ -418,6 +425,29 @@ def k_attention_bwd(q, ldq, k, ldk, v, ldv, o, ldo, dout, lddo, lse, D, dq, lddq
                                      lddv, T, S, hq, hkv, hd, _stream(stream)), what="lst_k_attention_bwd")
 
 
+def attention_window_scratch(T, S, hq, hkv, hd, window, sinks) -> int:
+    """fp32 values of scratch that k_attention_window_bwd needs (host only)."""
+    n = int(lib().lst_k_attention_window_scratch(T, S, hq, hkv, hd, window, sinks))
+    _check(1 if n < 0 else 0, what="lst_k_attention_window_scratch")
+    return n
+
+
+def k_attention_window_fwd(q, ldq, k, ldk, v, ldv, o, ldo, lse, T, S, hq, hkv, hd, window, sinks, stream=None):
+    """Causal attention in which query i sees key j <= i when i - j < window or j < sinks."""
+    _check(lib().lst_k_attention_window_fwd(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(o), ldo, _ptr(lse), T, S,
+                                            hq, hkv, hd, window, sinks, _stream(stream)),
+           what="lst_k_attention_window_fwd")
+
+
+def k_attention_window_bwd(q, ldq, k, ldk, v, ldv, o, ldo, dout, lddo, lse, scratch, dq, lddq, dk, lddk, dv, lddv,
+                           T, S, hq, hkv, hd, window, sinks, stream=None):
+    """scratch: fp32 [attention_window_scratch(...)]."""
+    _check(lib().lst_k_attention_window_bwd(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(o), ldo, _ptr(dout), lddo,
+                                            _ptr(lse), _ptr(scratch), _ptr(dq), lddq, _ptr(dk), lddk, _ptr(dv), lddv,
+                                            T, S, hq, hkv, hd, window, sinks, _stream(stream)),
+           what="lst_k_attention_window_bwd")
+
+
 def k_rmsnorm_fwd(x, g, T, d, eps, y, rstd, stream=None):
     _check(lib().lst_k_rmsnorm_fwd(_ptr(x), _ptr(g), T, d, eps, _ptr(y), _ptr(rstd), _stream(stream)),
            what="lst_k_rmsnorm_fwd")
@@ -450,6 +480,33 @@ def k_swiglu_bwd(dm, gu, T, F, dgu, stream=None):
 def k_cross_entropy(logits, T, V, targets, inv_T, loss_rows, dlogits, stream=None):
     _check(lib().lst_k_cross_entropy(_ptr(logits), T, V, _ptr(targets), inv_T, _ptr(loss_rows),
                                      _ptr(dlogits), _stream(stream)), what="lst_k_cross_entropy")
+
+
+POLICY_TOKEN_MEAN, POLICY_SEQ_MEAN, POLICY_FIXED = 0, 1, 2
+
+
+class Policy(C.Structure):
+    """lst_policy: the clip range, the KL weight, the normalisation (POLICY_*), the advantages' layout."""
+    _fields_ = [("clip_lo", C.c_float), ("clip_hi", C.c_float), ("kl_beta", C.c_float), ("norm", C.c_int32),
+                ("adv_per_seq", C.c_int32)]
+
+
+def policy_scratch(T, S) -> int:
+    """fp32 values of scratch that k_policy_loss needs (host only)."""
+    n = int(lib().lst_k_policy_scratch(T, S))
+    _check(1 if n < 0 else 0, what="lst_k_policy_scratch")
+    return n
+
+
+def k_policy_loss(logits, T, V, targets, S, adv, logp, out, scratch, dlogits=None, old_logp=None, ref_logp=None,
+                  mask=None, clip_lo=0.2, clip_hi=0.2, kl_beta=0.0, norm=POLICY_TOKEN_MEAN, adv_per_seq=False,
+                  stream=None):
+    """Clipped policy loss: out [4] (loss, kl, clipped, ratio), logp [T] and, when given, dlogits bf16
+    [T, V]; scratch: fp32 [policy_scratch(T, S)]."""
+    cfg = Policy(clip_lo, clip_hi, kl_beta, norm, int(bool(adv_per_seq)))
+    _check(lib().lst_k_policy_loss(_ptr(logits), T, V, _ptr(targets), S, _ptr(old_logp), _ptr(ref_logp), _ptr(adv),
+                                   _ptr(mask), C.byref(cfg), _ptr(logp), _ptr(out), _ptr(dlogits), _ptr(scratch),
+                                   _stream(stream)), what="lst_k_policy_loss")
 
 
 def k_lora_skinny(X, ldx, T, K, Bop, ldb, b_mn, KP, s, Us, stream=None):

@@ -6,6 +6,8 @@
 #include "lora.cuh"
 #include "nf4.cuh"
 #include "ops.cuh"
+#include "policy.cuh"
+#include "window.cuh"
 
 #include <atomic>
 
@@ -19,6 +21,8 @@ namespace {
 inline cudaStream_t S(void* s) { return static_cast<cudaStream_t>(s); }
 inline const bf16* B16(const uint16_t* p) { return reinterpret_cast<const bf16*>(p); }
 inline bf16* B16(uint16_t* p) { return reinterpret_cast<bf16*>(p); }
+inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool row8(const void* p, int64_t ld, int64_t cols) { return al16(p) && ld % 8 == 0 && ld >= cols; }
 inline lst_status st(cudaError_t e) {
   if (e == cudaSuccess) return LST_OK;
   cudaGetLastError();
@@ -173,6 +177,68 @@ lst_status lst_k_attention_bwd(const uint16_t* q, int64_t ldq, const uint16_t* k
   return st(attention_bwd(a, S(stream)));
 }
 
+int64_t lst_k_attention_window_scratch(int64_t T, int32_t Sq, int32_t hq, int32_t hkv, int32_t hd, int32_t window,
+                                       int32_t sinks) {
+  if (!window_shape_ok(T, Sq, hq, hkv, hd, window, sinks)) return -1;
+  return window_scratch(T, Sq, hq, hkv, hd, window, sinks);
+}
+
+lst_status lst_k_attention_window_fwd(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,
+                                      int64_t ldv, uint16_t* o, int64_t ldo, float* lse, int64_t T, int32_t Sq,
+                                      int32_t hq, int32_t hkv, int32_t hd, int32_t window, int32_t sinks,
+                                      void* stream) {
+  if (!q || !k || !v || !o || !lse || !window_shape_ok(T, Sq, hq, hkv, hd, window, sinks)) return LST_ERR_ARG;
+  const int64_t cq = (int64_t)hq * hd, ck = (int64_t)hkv * hd;
+  if (!row8(q, ldq, cq) || !row8(k, ldk, ck) || !row8(v, ldv, ck) || !row8(o, ldo, cq)) return LST_ERR_ARG;
+  WinArgs a;
+  static_cast<AttnArgs&>(a) = AttnArgs{B16(q), B16(k), B16(v), B16(o), lse, nullptr, ldq, ldk, ldv, ldo, T, Sq, hq, hkv, hd,
+                                       1.0f / sqrtf((float)hd)};
+  a.window = window;
+  a.sinks = sinks;
+  return st(window_fwd(a, S(stream)));
+}
+
+lst_status lst_k_attention_window_bwd(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v,
+                                      int64_t ldv, const uint16_t* o, int64_t ldo, const uint16_t* dout, int64_t lddo,
+                                      const float* lse, float* scratch, uint16_t* dq, int64_t lddq, uint16_t* dk,
+                                      int64_t lddk, uint16_t* dv, int64_t lddv, int64_t T, int32_t Sq, int32_t hq,
+                                      int32_t hkv, int32_t hd, int32_t window, int32_t sinks, void* stream) {
+  if (!lse || !scratch || !al16(scratch) || !window_shape_ok(T, Sq, hq, hkv, hd, window, sinks)) return LST_ERR_ARG;
+  if (!q || !k || !v || !o || !dout || !dq || !dk || !dv) return LST_ERR_ARG;
+  const int64_t cq = (int64_t)hq * hd, ck = (int64_t)hkv * hd;
+  if (!row8(q, ldq, cq) || !row8(k, ldk, ck) || !row8(v, ldv, ck) || !row8(o, ldo, cq) || !row8(dout, lddo, cq) ||
+      !row8(dq, lddq, cq) || !row8(dk, lddk, ck) || !row8(dv, lddv, ck))
+    return LST_ERR_ARG;
+  WinBwdArgs a;
+  a.q = B16(q);
+  a.k = B16(k);
+  a.v = B16(v);
+  a.o = B16(o);
+  a.dout = B16(dout);
+  a.lse = lse;
+  a.D = scratch;
+  a.dq = B16(dq);
+  a.dk = B16(dk);
+  a.dv = B16(dv);
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.ldo = ldo;
+  a.lddo = lddo;
+  a.lddq = lddq;
+  a.lddk = lddk;
+  a.lddv = lddv;
+  a.T = T;
+  a.S = Sq;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.hd = hd;
+  a.scale = 1.0f / sqrtf((float)hd);
+  a.window = window;
+  a.sinks = sinks;
+  return st(window_bwd(a, S(stream)));
+}
+
 lst_status lst_k_rmsnorm_fwd(const float* x, const float* g, int64_t T, int32_t d, float eps, uint16_t* y,
                              float* rstd, void* stream) {
   if (!x || !g || !y || !rstd || T <= 0 || d <= 0) return LST_ERR_ARG;
@@ -210,6 +276,22 @@ lst_status lst_k_cross_entropy(const float* logits, int64_t T, int32_t V, const 
                                float* loss_rows, uint16_t* dlogits, void* stream) {
   if (!logits || !targets || !loss_rows || !dlogits || T <= 0 || V <= 0) return LST_ERR_ARG;
   return st(cross_entropy(logits, T, V, targets, inv_T, loss_rows, B16(dlogits), S(stream)));
+}
+
+int64_t lst_k_policy_scratch(int64_t T, int32_t Sq) {
+  return T <= 0 || Sq <= 0 || T % Sq ? -1 : policy_scratch(T, Sq);
+}
+
+lst_status lst_k_policy_loss(const float* logits, int64_t T, int32_t V, const int32_t* targets, int32_t Sq,
+                             const float* old_logp, const float* ref_logp, const float* adv, const int32_t* mask,
+                             const lst_policy* cfg, float* logp, float* out, uint16_t* dlogits, float* scratch,
+                             void* stream) {
+  if (!logits || !targets || !adv || !cfg || !logp || !out || !scratch || !al16(scratch)) return LST_ERR_ARG;
+  const PolicyArgs a{logits, T, V, Sq, targets, old_logp, ref_logp, adv, mask, cfg->clip_lo, cfg->clip_hi, cfg->kl_beta,
+                     cfg->norm, cfg->adv_per_seq ? 1 : 0, logp, out, B16(dlogits), scratch};
+  if (!policy_args_ok(a)) return LST_ERR_ARG;
+  const cudaError_t e = policy_begin(a, S(stream));
+  return st(e != cudaSuccess ? e : policy_rows(a, 0, T, S(stream)));
 }
 
 lst_status lst_k_lora_skinny(const uint16_t* X, int64_t ldx, int64_t T, int32_t K, const uint16_t* Bop, int64_t ldb,

@@ -79,15 +79,23 @@ def rope_bwd(dy, cos, sin, batch, seq):
     return np.concatenate([d1 * c + d2 * s, d2 * c - d1 * s], axis=-1)
 
 
-def attention(q, k, v, batch, seq):
+def visible(seq, window=0, sinks=0):
+    """[seq, seq] truth values: query i sees key j. Causal (window 0), or under a sliding window with
+    sinks: j <= i and (i - j < window or j < sinks)."""
+    i, j = np.arange(seq)[:, None], np.arange(seq)[None, :]
+    return (j <= i) & ((i - j < window) | (j < sinks) if window > 0 else True)
+
+
+def attention(q, k, v, batch, seq, window=0, sinks=0):
     """Causal GQA attention. q [T, hq, hd], k/v [T, hkv, hd]; query head h reads kv head
-    h // (hq/hkv); scale 1/sqrt(hd). Returns (o [T, hq, hd], P [B, hq, S, S])."""
+    h // (hq/hkv); scale 1/sqrt(hd); window > 0: under a window with sinks (``visible``). Returns
+    (o [T, hq, hd], P [B, hq, S, S]); ``attention_bwd`` takes the mask from P."""
     T, hq, hd = q.shape
     hkv = k.shape[1]
     grp = hq // hkv
     o = np.zeros_like(q)
     P = np.zeros((batch, hq, seq, seq))
-    mask = np.triu(np.ones((seq, seq), dtype=bool), 1)
+    mask = ~visible(seq, window, sinks)
     for b in range(batch):
         rows = slice(b * seq, (b + 1) * seq)
         for h in range(hq):
@@ -202,7 +210,8 @@ def _round_bf16(x):
 
 
 class Shape:
-    def __init__(self, wl, bf16_acts: bool = False):
+    def __init__(self, wl, bf16_acts: bool = False, window: int = 0, sinks: int = 0):
+        self.window, self.sinks = window, sinks
         self.rb = _round_bf16 if bf16_acts else _identity
         self.batch, self.seq = wl.batch, wl.seq
         self.hq, self.hkv, self.hd = wl.n_heads, wl.n_kv_heads, wl.head_dim
@@ -226,7 +235,7 @@ def layer_fwd(x, Wt, lora, sh: Shape):
     q = rb(rope(c["q_pre"].reshape(T, sh.hq, sh.hd), sh.cos, sh.sin, sh.batch, sh.seq))
     k = rb(rope(c["k_pre"].reshape(T, sh.hkv, sh.hd), sh.cos, sh.sin, sh.batch, sh.seq))
     v = rb(c["v_pre"].reshape(T, sh.hkv, sh.hd))
-    o, P = attention(q, k, v, sh.batch, sh.seq)
+    o, P = attention(q, k, v, sh.batch, sh.seq, sh.window, sh.sinks)
     c.update(q=q, k=k, v=v, P=P, o=rb(o.reshape(T, -1)))
     ao, c["u_o"] = lora_linear(c["o"], Wt["W"]["o"], *lora["o"], sh.s)
     h = x + ao
@@ -307,8 +316,8 @@ def _lora64(raw):
 
 
 def step(wl, raw_layers, blobs=None, head=None, tokens=None, targets=None, x_in=None, G=None,
-         schedule="resident", lora=None, bf16_acts=False):
-    """Loss and LoRA gradients of one step.
+         schedule="resident", lora=None, bf16_acts=False, window=0, sinks=0):
+    """Loss and LoRA gradients of one step (window > 0: attention under a window with sinks).
 
     raw_layers: per layer the synthetic dict (only A/B are read here; base comes from ``blobs``).
     blobs: per layer ``pack_layer`` output (built here when None).
@@ -320,7 +329,7 @@ def step(wl, raw_layers, blobs=None, head=None, tokens=None, targets=None, x_in=
     Returns dict(loss, grads[layer][proj] = (dA, dB), logits or None, reads).
     """
     L = wl.n_layers
-    sh = Shape(wl, bf16_acts)
+    sh = Shape(wl, bf16_acts, window, sinks)
     if blobs is None:
         blobs = [pack_layer(raw_layers[i], wl.base_format) for i in range(L)]
     if lora is None:
@@ -544,3 +553,91 @@ def pref_step(wl, raw_layers, head, tokens, targets, npairs, kind, mask=None, bl
     for i in reversed(range(L)):
         dx, grads[i] = layer_bwd(dx, caches[i], Ws[i], lora[i], sh)
     return {"loss": loss, "grads": grads, "pi": pi}
+
+
+# ------------------------------------------------------------------------------------------
+# policy step: clipped policy loss with a KL term to the base with the adapters switched off
+# ------------------------------------------------------------------------------------------
+# The clipped surrogate of Schulman et al., "Proximal Policy Optimization Algorithms" (2017), on
+# per-token ratios, with the per-token KL estimate of Shao et al., "DeepSeekMath: Pushing the Limits
+# of Mathematical Reasoning in Open Language Models" (2024), which takes the loss to advantages that
+# are known per sampled answer. The reference model is the DPO step's: the same base, adapters off.
+
+def policy_weights(mask, nseq, seq, norm):
+    """w_t per token: "token" m / sum m, "seq" m / (nseq sum_seq m), "fixed" m / T."""
+    m = (np.asarray(mask) != 0).astype(F64).reshape(nseq, seq)
+    if norm == "token":
+        w = m / max(m.sum(), 1.0)
+    elif norm == "seq":
+        w = m / np.maximum(m.sum(axis=1, keepdims=True), 1.0) / nseq
+    elif norm == "fixed":
+        w = m / m.size
+    else:
+        raise ValueError(norm)
+    return w.reshape(-1)
+
+
+def policy_loss(logp, old, ref, adv, w, lo, hi, beta):
+    """(out [4], d loss / d logp [T]) from per-token log-probabilities and advantages; old None:
+    ratio 1; ref None: no KL term. out: sums of w times loss, kl, [clipped], ratio."""
+    r = np.exp(logp - old) if old is not None else np.ones_like(logp)
+    inner, outer = r * adv, np.clip(r, 1.0 - lo, 1.0 + hi) * adv
+    cut = inner > outer
+    d = ref - logp if ref is not None else np.zeros_like(logp)
+    kl = np.expm1(d) - d
+    token = -np.minimum(inner, outer) + beta * kl
+    slope = np.where(cut, 0.0, -inner) - beta * np.expm1(d)
+    on = w > 0
+    out = np.array([np.sum((w * a)[on]) for a in (token, kl, cut.astype(F64), r)])
+    return out, np.where(on, w * slope, 0.0)
+
+
+def policy_dlogits(logits, targets, old, ref, adv, mask, nseq, seq, norm, lo, hi, beta):
+    """(out, dL/dlogits, logp) of the policy loss as a function of the logits [nseq*seq, V]."""
+    T = logits.shape[0]
+    on = np.asarray(mask) != 0
+    mx = logits.max(axis=1, keepdims=True)
+    lse = (mx + np.log(np.exp(logits - mx).sum(axis=1, keepdims=True)))[:, 0]
+    y = np.where(on, targets, 0)
+    logp = logits[np.arange(T), y] - lse
+    a = np.repeat(adv, seq) if adv.shape[0] == nseq and seq > 1 else adv
+    out, g = policy_loss(logp, old, ref, a, policy_weights(mask, nseq, seq, norm), lo, hi, beta)
+    dlog = -np.exp(logits - lse[:, None]) * g[:, None]
+    dlog[np.arange(T), y] += g
+    return out, np.where(on[:, None], dlog, 0.0), np.where(on, logp, 0.0)
+
+
+def policy_step(wl, raw_layers, head, tokens, targets, adv, old=None, mask=None, norm="seq", lo=0.2, hi=0.2, beta=0.0,
+                bf16_acts=False, lora=None, window=0, sinks=0):
+    """Loss and LoRA gradients of one policy step on wl.batch sequences of wl.seq tokens. beta > 0:
+    the reference log-probabilities come from a pass with the adapters off.
+    Returns dict(out, grads, logp, ref)."""
+    L = wl.n_layers
+    sh = Shape(wl, bf16_acts, window, sinks)
+    blobs = [pack_layer(raw_layers[i], wl.base_format) for i in range(L)]
+    if lora is None:
+        lora = [_lora64(raw_layers[i]) for i in range(L)]
+    E, gf, H = (a.astype(F64) for a in head)
+    T = wl.batch * wl.seq
+    m = np.ones(T) if mask is None else np.asarray(mask, dtype=F64)
+    Ws = [unpack_blob(blobs[i]) for i in range(L)]
+
+    def head_logits(xL):
+        n, r = rmsnorm(xL, gf, wl.rms_eps)
+        return sh.rb(n) @ H.T, r
+
+    ref = None
+    if beta > 0:
+        off = [{p: (a, np.zeros_like(b)) for p, (a, b) in lo_.items()} for lo_ in lora]
+        lr = head_logits(_forward(E[tokens], Ws, off, sh)[0])[0]
+        mx = lr.max(axis=1, keepdims=True)
+        ref = lr[np.arange(T), targets] - (mx + np.log(np.exp(lr - mx).sum(axis=1, keepdims=True)))[:, 0]
+    xL, caches = _forward(E[tokens], Ws, lora, sh)
+    logits, r = head_logits(xL)
+    out, dlog, logp = policy_dlogits(logits, targets, old, ref, np.asarray(adv, dtype=F64), m, wl.batch, wl.seq, norm,
+                                     lo, hi, beta)
+    dx = rmsnorm_bwd(sh.rb(dlog) @ H, xL, gf, r)
+    grads = [None] * L
+    for i in reversed(range(L)):
+        dx, grads[i] = layer_bwd(dx, caches[i], Ws[i], lora[i], sh)
+    return {"out": out, "grads": grads, "logp": logp, "ref": ref}
