@@ -2,15 +2,41 @@
 // of Schulman et al., "Proximal Policy Optimization Algorithms", 2017, with the per-token KL estimate
 // k3 of Shao et al., "DeepSeekMath", 2024; formulas in policy.cuh). Its gradient:
 //   dl/dlogp = -r A [u is r A] + beta (1 - exp(ref - logp)),  dlogits = w dl/dlogp (onehot(y) - softmax(x)).
-// One CTA per row reads it twice: maximum and sum of exponentials, then dlogits.
+// Each logit crosses HBM once: a cluster of CTAs holds a row in registers from its load to the store of
+// dlogits (k_policy_cluster); only rows too long for that are read twice (k_policy_rows).
 #include "common.cuh"
 #include "pdl.cuh"
+#include "ex2.cuh"
 #include "policy.cuh"
+
+#include <algorithm>
 
 namespace lst {
 namespace {
 
 using bf16 = __nv_bfloat16;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(uintptr_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"((uint64_t)dst), "r"(smem_u32(src)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {  // this thread's bulk stores have been made
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+// 8 bytes into a cluster CTA's shared memory, counted by the mbarrier there
+__device__ __forceinline__ void st_async_f2(uint32_t dst, float x, float y, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(dst), "f"(x),
+               "f"(y), "r"(bar)
+               : "memory");
+}
 
 // scratch: [0] rows done so far (as unsigned), then 4 floats a row, then the weight of each sequence's tokens
 __host__ __device__ inline float* row_terms(float* scratch) { return scratch + 4; }
@@ -34,14 +60,13 @@ struct Token {
   float4 terms;
   float slope;
 };
-__device__ __forceinline__ Token policy_token(const PolicyArgs& a, int64_t t, float logp) {
-  const float A = a.adv[a.adv_per_seq ? t / a.S : t];
-  const float r = a.old_logp ? expf(logp - a.old_logp[t]) : 1.f;
+__device__ __forceinline__ Token policy_token(const PolicyArgs& a, float A, float old, float ref, float logp) {
+  const float r = a.old_logp ? expf(logp - old) : 1.f;
   const float in = r * A, cl = fminf(fmaxf(r, 1.f - a.lo), 1.f + a.hi) * A;
   const bool cut = in > cl;  // the clip lowers the surrogate: no gradient
   float kl = 0.f, dkl = 0.f;
   if (a.ref_logp) {
-    const float d = a.ref_logp[t] - logp;
+    const float d = ref - logp;
     kl = k3_term(d);
     dkl = -expm1f(d);
   }
@@ -79,21 +104,38 @@ __global__ void __launch_bounds__(1024) k_policy_weights(const int32_t* __restri
     for (int64_t b = threadIdx.x; b < nseq; b += blockDim.x) w[b] = common;
 }
 
-// The last CTA of the call adds the row terms in a fixed order (fp64) and writes out.
-__device__ __forceinline__ void finish_row(const PolicyArgs& a, int64_t t, float4 terms) {
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ bool named_all(int id, int threads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+// Once thread 0 has stored the terms of its `done` rows: the last CTA of the call to get here adds the
+// terms of all rows in a fixed order (fp64) and writes out. For the first nt threads of a CTA (whole
+// warps), all of them; part: 128 values of shared memory.
+__device__ __forceinline__ void finish_rows(const PolicyArgs& a, int done, int nt, double* part) {
   __shared__ bool last;
-  __shared__ double part[4][32];
   if (threadIdx.x == 0) {
-    reinterpret_cast<float4*>(row_terms(a.scratch))[t] = terms;
     __threadfence();
-    last = atomicAdd(reinterpret_cast<unsigned*>(a.scratch), 1u) + 1u == (unsigned)a.T;
+    last = done > 0 && atomicAdd(reinterpret_cast<unsigned*>(a.scratch), (unsigned)done) + (unsigned)done == (unsigned)a.T;
   }
-  __syncthreads();
+  named_sync(1, nt);
   if (!last) return;
   __threadfence();
   const float4* rows = reinterpret_cast<const float4*>(row_terms(a.scratch));
   double s[4] = {0, 0, 0, 0};
-  for (int64_t i = threadIdx.x; i < a.T; i += blockDim.x) {
+  for (int64_t i = threadIdx.x; i < a.T; i += nt) {
     const float4 v = __ldcg(rows + i);
     s[0] += v.x;
     s[1] += v.y;
@@ -103,21 +145,283 @@ __device__ __forceinline__ void finish_row(const PolicyArgs& a, int64_t t, float
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     for (int o = 16; o > 0; o >>= 1) s[e] += __shfl_xor_sync(0xffffffffu, s[e], o);
-    if ((threadIdx.x & 31) == 0) part[e][threadIdx.x >> 5] = s[e];
+    if ((threadIdx.x & 31) == 0) part[e * 32 + (threadIdx.x >> 5)] = s[e];
   }
-  __syncthreads();
+  named_sync(1, nt);
   if (threadIdx.x < 4) {
     double v = 0;
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v += part[threadIdx.x][i];
+    for (int i = 0; i < (nt >> 5); ++i) v += part[threadIdx.x * 32 + i];
     a.out[threadIdx.x] = (float)v;
   }
 }
 
+// One counted row's scalars, brought in ahead of it; lrow < 0 ends the rows.
+struct RowInfo {
+  int64_t lrow;
+  int y;
+  float xy, adv, old, ref, w;
+};
+constexpr int kZeroBytes = 1024;
+
+// Persistent clusters of cs CTAs, cluster g taking rows g, g + clusters, ... CTA z owns slots
+// [z * slice, (z + 1) * slice) of a row's 16-byte slots (slot i: logits 4 i - off .. 4 i - off + 3, off =
+// how far the row starts behind a 16-byte boundary).
+//  - The last warp is the producer: it reads the scalars of 32 rows at once, a lane each. A row that
+//    does not count it finishes by itself, by bulk stores from a kilobyte of zeros. A counted row's slice it
+//    brings into shared memory by bulk copies, in two halves of a ring of three. The consumers take a
+//    half to registers at once, so up to one and a half rows are in flight under a row's arithmetic,
+//    exchange and stores.
+//  - Consumer thread i holds slots i, i + consumers, ... of each half: NV of them, 4 NV logits, NV large
+//    and the threads few, so that two slices fit an SM's registers without spills. With m its own
+//    maximum it forms e = 2^((x - m) log2 e) once; maxima and sums are merged by warp, CTA and cluster
+//    (st.async of each CTA's pair into its peers, onto their mbarrier), in a fixed order; the row's
+//    factor coef 2^((m - lse) log2 e) then turns e into dlogits with one product.
+// Each logit crosses HBM once and takes one exponential. Bound by HBM: 4 + 2 bytes a logit, 2 bytes on
+// rows that do not count.
+template <int NV, int THREADS, int PER_SM>
+__global__ void __launch_bounds__(THREADS, PER_SM)
+k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice) {
+  static_assert(NV % 2 == 0 && kZeroBytes >= 128 * 8, "two halves; the zeros' space is reused");
+  extern __shared__ __align__(16) float ring[];  // three halves of a slice
+  __shared__ __align__(16) uint8_t zeros[kZeroBytes];
+  __shared__ uint64_t full[3], empty[3], pair_bar[2];
+  // by counted row: rewritten for the fourth row after it, which waits for a buffer that the consumers
+  // free behind this row
+  __shared__ RowInfo info[4];
+  __shared__ float2 pair[2][8];  // (max, sum) of each CTA of the cluster, by row parity
+  __shared__ float2 wpair[32];   // of each warp of this CTA
+  __shared__ float2 factor;      // lse and the row's coefficient
+  const int cs = (int)cluster_size_x(), z = (int)cluster_rank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nc = (int)blockDim.x - 32, ncw = nc >> 5;  // consumers
+  const int half = (slice + 1) / 2;
+  const int64_t clusters = gridDim.x / cs, first = blockIdx.x / cs;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], (uint32_t)ncw);
+    }
+    mbar_init(&pair_bar[0], 1);
+    mbar_init(&pair_bar[1], 1);
+    fence_mbar_init();
+  }
+  for (int i = threadIdx.x; i < kZeroBytes / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(zeros)[i] = 0;
+  fence_proxy_async();  // the zeros are read by bulk stores
+  __syncthreads();
+  cluster_sync_all();  // every CTA's barriers are set up before a peer's pair can arrive
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == ncw) {  // producer
+    int it = 0, g = 0;  // counted rows, halves
+    bool ok = true;
+    const auto claim = [&] {  // the next buffer of the ring, once it is free
+      if (g >= 3 && !__all_sync(0xffffffffu, mbar_wait(&empty[g % 3], (g / 3 - 1) & 1))) ok = false;
+      return ok;
+    };
+    for (int64_t base = first; base < rows && ok; base += 32 * clusters) {
+      const int64_t mine = base + lane * clusters;
+      RowInfo r{mine, 0, 0.f, 0.f, 0.f, 0.f, 0.f};
+      bool live = false;
+      if (mine < rows) {
+        const int64_t t = row0 + mine;
+        r.y = a.y[t];
+        live = !a.mask || a.mask[t] != 0;
+        if (live && (r.y < 0 || r.y >= a.V)) {
+          if (z == 0) dev_fail(DEV_ERR_BAD_INDEX);
+          live = false;
+        }
+        if (live) {
+          r.xy = a.logits[mine * a.V + r.y];
+          r.adv = a.adv[a.adv_per_seq ? t / a.S : t];
+          r.old = a.old_logp ? a.old_logp[t] : 0.f;
+          r.ref = a.ref_logp ? a.ref_logp[t] : 0.f;
+          r.w = seq_weight(a.scratch, a.T)[t / a.S];
+        } else if (z == 0) {
+          a.logp[t] = 0.f;
+          reinterpret_cast<float4*>(row_terms(a.scratch))[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+      const uint32_t lives = __ballot_sync(0xffffffffu, live);
+      for (int i = 0; i < 32 && ok; ++i) {
+        const int64_t lrow = base + i * clusters;
+        if (lrow >= rows) break;
+        if (!(lives >> i & 1)) {  // zeros to this CTA's part of the row, whole 16 bytes of it by bulk stores
+          if (a.dlog) {
+            const int64_t per = (a.V + cs - 1) / cs;
+            const bf16* d0 = a.dlog + lrow * a.V + min((int64_t)a.V, z * per);
+            const bf16* d1 = a.dlog + lrow * a.V + min((int64_t)a.V, (z + 1) * per);
+            const uintptr_t p0 = reinterpret_cast<uintptr_t>(d0), p1 = reinterpret_cast<uintptr_t>(d1);
+            uintptr_t q0 = (p0 + 15) & ~uintptr_t(15), q1 = p1 & ~uintptr_t(15);
+            if (q0 > q1) q0 = q1 = p1;
+            if (p0 + 2 * lane < min(q0, p1)) *reinterpret_cast<bf16*>(p0 + 2 * lane) = __float2bfloat16_rn(0.f);
+            if (max(q1, p0) + 2 * lane < p1) *reinterpret_cast<bf16*>(max(q1, p0) + 2 * lane) = __float2bfloat16_rn(0.f);
+            for (uintptr_t q = q0 + lane * kZeroBytes; q < q1; q += 32 * kZeroBytes)
+              bulk_store(q, zeros, (uint32_t)min((uintptr_t)kZeroBytes, q1 - q));
+          }
+          continue;
+        }
+        const float* x = a.logits + lrow * a.V;
+        const int off = (int)(reinterpret_cast<uintptr_t>(x) >> 2) & 3, end = (a.V + off + 3) / 4;
+        for (int h = 0; h < 2 && claim(); ++h, ++g) {
+          const int k = g % 3;
+          if (h == 0 && lane == i) info[it & 3] = r;
+          float* buf = ring + 4 * k * half;
+          const int b = z * slice + h * half, e = min(min(b + half, (z + 1) * slice), end);
+          // [lo, hi): slots without a logit of a neighbouring row; the row's first and last slot may have
+          // one and are filled in by hand then
+          const int lo = max(b, off ? 1 : 0), hi = min(e, (a.V + off) / 4);
+          for (int c = b; c < e; c = c < lo ? lo : max(c + 1, hi)) {
+            if (c >= lo && c < hi) continue;
+            const int at = 4 * c - off + lane;
+            if (lane < 4) buf[4 * (c - b) + lane] = at >= 0 && at < a.V ? x[at] : -INFINITY;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if (hi > lo) {
+              mbar_arrive_expect_tx(&full[k], (uint32_t)(hi - lo) * 16);
+              const int q = (hi - lo + 1) / 2;
+              for (int c = lo; c < hi; c += q)
+                bulk_load(buf + 4 * (c - b), x + (4 * c - off), (uint32_t)min(q, hi - c) * 16, &full[k]);
+            } else {
+              mbar_arrive(&full[k]);
+            }
+          }
+        }
+        ++it;
+      }
+    }
+    bulk_store_wait();
+    if (ok && claim()) {  // (the zeros are the consumers' from here on)
+      if (lane == 0) {
+        info[it & 3].lrow = -1;
+        mbar_arrive(&full[g % 3]);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+    return;
+  }
+
+  int it = 0, g = 0;  // counted rows, halves
+  bool ok = true;
+  for (; ok; ++it) {
+    if (!mbar_wait(&full[g % 3], (g / 3) & 1)) {  // for every consumer alike: the phase does not end
+      ok = false;
+      break;
+    }
+    const int64_t lrow = info[it & 3].lrow, t = row0 + lrow;
+    if (lrow < 0) break;
+    const int y = info[it & 3].y;
+    const float* x = a.logits + lrow * a.V;
+    bf16* d = a.dlog ? a.dlog + lrow * a.V : nullptr;
+    const int off = (int)(reinterpret_cast<uintptr_t>(x) >> 2) & 3;
+    const int b = z * slice, s1 = min((a.V + off + 3) / 4, b + slice);
+    const bool dvec = (reinterpret_cast<uintptr_t>(d - off) & 7) == 0;
+    float v[4 * NV];
+    // this thread's slots: those n < NV / 2 with n * nc < mine[0], and as many of the second half
+    const int mine[2] = {min(half, s1 - b) - (int)threadIdx.x, s1 - b - half - (int)threadIdx.x};
+#pragma unroll
+    for (int h = 0; h < 2; ++h, ++g) {
+      if (h == 1 && !mbar_wait(&full[g % 3], (g / 3) & 1)) ok = false;
+      const float4* src = reinterpret_cast<const float4*>(ring + 4 * (g % 3) * half) + threadIdx.x;
+#pragma unroll
+      for (int n = 0; n < NV / 2; ++n) {
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (n * nc < mine[h]) q = src[n * nc];
+        float* o = v + 4 * (h * (NV / 2) + n);
+        o[0] = q.x;
+        o[1] = q.y;
+        o[2] = q.z;
+        o[3] = q.w;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[g % 3]);
+    }
+    // everything in units of log2: e = 2^(x log2 e - m), m the thread's rounded maximum; what matters is
+    // that one m is used throughout (a thread without a finite logit takes 0 and adds zeros)
+    float m4[4] = {v[0], v[1], v[2], v[3]}, s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = 4; n < 4 * NV; ++n) m4[n & 3] = fmaxf(m4[n & 3], v[n]);
+    float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    m = m > -INFINITY ? m * kLog2e : 0.f;
+#pragma unroll
+    for (int n = 0; n < 4 * NV; ++n) {
+      v[n] = ex2_approx(fmaf(v[n], kLog2e, -m));
+      s4[n & 3] += v[n];
+    }
+    const float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+    if (s == 0.f) m = -INFINITY;
+    const float wm = warp_max(m);
+    const float ws = warp_sum(m > -INFINITY ? s * ex2_approx(m - wm) : s);
+    if (lane == 0) wpair[warp] = make_float2(wm, ws);
+    named_sync(1, nc);
+    if (warp == 0) {
+      float2 p = lane < ncw ? wpair[lane] : make_float2(-INFINITY, 0.f);
+      float rm = warp_max(p.x);
+      float rs = warp_sum(p.x > -INFINITY ? p.y * ex2_approx(p.x - rm) : p.y);
+      if (cs > 1) {
+        const int k = it & 1;
+        if (lane == 0) mbar_arrive_expect_tx(&pair_bar[k], (uint32_t)cs * 8);
+        if (lane < cs)
+          st_async_f2(cluster_map(smem_u32(&pair[k][z]), (uint32_t)lane), rm, rs,
+                      cluster_map(smem_u32(&pair_bar[k]), (uint32_t)lane));
+        if (!mbar_wait(&pair_bar[k], (it >> 1) & 1)) ok = false;
+        p = lane < cs ? pair[k][lane] : make_float2(-INFINITY, 0.f);
+        rm = warp_max(p.x);
+        rs = warp_sum(p.x > -INFINITY ? p.y * ex2_approx(p.x - rm) : p.y);
+      }
+      if (lane == 0) {
+        const RowInfo& r = info[it & 3];
+        const float l2 = log2f(rs), logp = (fmaf(r.xy, kLog2e, -rm) - l2) * kLn2;
+        const Token k = policy_token(a, r.adv, r.old, r.ref, logp);
+        factor = make_float2(rm + l2, -r.w * k.slope);
+        if (z == 0) {
+          a.logp[t] = logp;
+          reinterpret_cast<float4*>(row_terms(a.scratch))[t] =
+              make_float4(r.w * k.terms.x, r.w * k.terms.y, r.w * k.terms.z, r.w * k.terms.w);
+        }
+      }
+    }
+    ok = named_all(1, nc, ok);  // a lost pair ends the loop for every consumer
+    if (!d) continue;
+    // no slot here holds a neighbour's logits, and the stores are aligned: nothing to look at a slot
+    const bool whole = dvec && (b > 0 || off == 0) && 4 * s1 - off <= a.V;
+    const float lse2 = factor.x, coef = factor.y, f = coef * ex2_approx(m - lse2);
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int h = n / (NV / 2), k = (n - h * (NV / 2)) * nc;
+      if (k >= mine[h]) continue;
+      const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(v[4 * n] * f, v[4 * n + 1] * f),
+                                   __floats2bfloat162_rn(v[4 * n + 2] * f, v[4 * n + 3] * f)};
+      const int c = 4 * (b + h * half + k + (int)threadIdx.x) - off;
+      if (whole || (dvec && c >= 0 && c + 4 <= a.V)) {
+        *reinterpret_cast<uint2*>(d + c) = *reinterpret_cast<const uint2*>(w);
+      } else {
+        const bf16* q = reinterpret_cast<const bf16*>(w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e >= 0 && c + e < a.V) d[c + e] = q[e];
+      }
+    }
+    // the target's own element, by the thread that has just stored its slot
+    const int ys = (y + off) / 4 - b;
+    if (ys >= 0 && ys < slice && (ys < half ? ys : ys - half) % nc == (int)threadIdx.x)
+      d[y] = __float2bfloat16_rn(coef * (ex2_approx(fmaf(info[it & 3].xy, kLog2e, -lse2)) - 1.f));
+  }
+  if (z == 0 && ok)
+    finish_rows(a, (int)((rows - first + clusters - 1) / clusters), nc, reinterpret_cast<double*>(zeros));
+  __syncwarp();
+  cluster_sync_all();  // no CTA leaves before its peers have their pairs
+}
+
+// Rows longer than a cluster's registers (V above 300,000): one CTA a row, read twice.
 __global__ void __launch_bounds__(512) k_policy_rows(const PolicyArgs a, int64_t row0) {
   pdl_wait();
   pdl_trigger();
   __shared__ float red[16];
   __shared__ float coef_s;
+  __shared__ double part[128];
   const int64_t lrow = blockIdx.x, t = row0 + lrow;
   const float* x = a.logits + lrow * a.V;
   bf16* d = a.dlog ? a.dlog + lrow * a.V : nullptr;
@@ -128,8 +432,11 @@ __global__ void __launch_bounds__(512) k_policy_rows(const PolicyArgs a, int64_t
   if (!counted || bad) {
     if (d)
       for (int c = threadIdx.x; c < a.V; c += blockDim.x) d[c] = __float2bfloat16_rn(0.f);
-    if (threadIdx.x == 0) a.logp[t] = 0.f;
-    finish_row(a, t, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (threadIdx.x == 0) {
+      a.logp[t] = 0.f;
+      reinterpret_cast<float4*>(row_terms(a.scratch))[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    finish_rows(a, 1, blockDim.x, part);
     return;
   }
   float m = -INFINITY, s = 0.f;
@@ -146,14 +453,15 @@ __global__ void __launch_bounds__(512) k_policy_rows(const PolicyArgs a, int64_t
   s = 0.f;
   for (int i = 0; i < (int)(blockDim.x >> 5); ++i) s += red[i];
   const float ls = logf(s);
-  float4 terms;
   if (threadIdx.x == 0) {
     const float logp = (x[y] - m) - ls;
-    const Token k = policy_token(a, t, logp);
+    const Token k = policy_token(a, a.adv[a.adv_per_seq ? t / a.S : t], a.old_logp ? a.old_logp[t] : 0.f,
+                                 a.ref_logp ? a.ref_logp[t] : 0.f, logp);
     const float w = seq_weight(a.scratch, a.T)[t / a.S];
     a.logp[t] = logp;
     coef_s = -w * k.slope;
-    terms = make_float4(w * k.terms.x, w * k.terms.y, w * k.terms.z, w * k.terms.w);
+    reinterpret_cast<float4*>(row_terms(a.scratch))[t] =
+        make_float4(w * k.terms.x, w * k.terms.y, w * k.terms.z, w * k.terms.w);
   }
   __syncthreads();
   if (d) {
@@ -163,7 +471,48 @@ __global__ void __launch_bounds__(512) k_policy_rows(const PolicyArgs a, int64_t
       d[c] = __float2bfloat16_rn(coef * (c == y ? p - 1.f : p));
     }
   }
-  finish_row(a, t, terms);
+  finish_rows(a, 1, blockDim.x, part);
+}
+
+// As many clusters as are resident at once (they take the rows in turn), at most one a row.
+template <int NV, int THREADS, int PER_SM>
+cudaError_t launch_cluster(const PolicyArgs& a, int64_t row0, int64_t rows, int cs, int slice, cudaStream_t s) {
+  const auto kernel = k_policy_cluster<NV, THREADS, PER_SM>;
+  const int half = (slice + 1) / 2;
+  const int threads = std::max(32, ((half + NV / 2 - 1) / (NV / 2) + 31) / 32 * 32) + 32, smem = 3 * half * 16;
+  static std::atomic<unsigned long long> attr_done{0};
+  if (!done_on_device(attr_done)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               std::min((THREADS - 32) * NV / 2 * 3 * 16, 224 * 1024));
+    if (e != cudaSuccess) return e;
+    mark_done_on_device(attr_done);
+  }
+  struct Fit {
+    int device, cs, slice, clusters;
+  };
+  static thread_local Fit fit{-1, 0, 0, 0};  // of this thread's last call
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (fit.device != dev || fit.cs != cs || fit.slice != slice) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)cs);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cs;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+    fit = Fit{dev, cs, slice, std::max(1, n)};
+  }
+  const int64_t clusters = std::min<int64_t>(rows, fit.clusters);
+  return launch_k(kernel, dim3((unsigned)(clusters * cs)), dim3((unsigned)threads), (size_t)smem, s, (unsigned)cs, a, row0,
+                  rows, slice);
 }
 
 }  // namespace
@@ -185,7 +534,18 @@ cudaError_t policy_begin(const PolicyArgs& a, cudaStream_t s) {
 
 cudaError_t policy_rows(const PolicyArgs& a, int64_t row0, int64_t rows, cudaStream_t s) {
   if (!policy_args_ok(a) || row0 < 0 || rows <= 0 || row0 + rows > a.T) return cudaErrorInvalidValue;
-  const cudaError_t e = launch_k(k_policy_rows, dim3((unsigned)rows), dim3(512), 0, s, 0, a, row0);
+  // A CTA takes up to 4750 slots (224 consumers of 22, three half slices of shared memory), two CTAs an SM. A few rows are spread further, so
+  // that every SM has some of them, and a shorter slice is a shorter chain for a row.
+  const int slots = (a.V + 6) / 4;
+  int cs = 1;
+  while (cs < 8 && ((slots + cs - 1) / cs > 4750 || (rows * cs < 2 * device_sm_count() && slots / cs > 1024))) cs *= 2;
+  const int slice = (slots + cs - 1) / cs;
+  cudaError_t e;
+  if (slice <= 512) e = launch_cluster<2, 288, 4>(a, row0, rows, cs, slice, s);
+  else if (slice <= 1536) e = launch_cluster<6, 288, 4>(a, row0, rows, cs, slice, s);
+  else if (slice <= 4750) e = launch_cluster<22, 256, 2>(a, row0, rows, cs, slice, s);
+  else if (slice <= 9400) e = launch_cluster<22, 512, 1>(a, row0, rows, cs, slice, s);
+  else e = launch_k(k_policy_rows, dim3((unsigned)rows), dim3(512), 0, s, 0, a, row0);
   note_launch(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
