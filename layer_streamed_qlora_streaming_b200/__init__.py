@@ -146,11 +146,13 @@ def _ptr(x) -> int | None:
         return None
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
+    data_ptr = getattr(x, "data_ptr", None)
+    if data_ptr is not None:
         # row-strided views are fine: every entry point takes explicit leading dimensions
-        if x.dim() > 0 and x.stride(-1) != 1:
+        stride = x.stride()
+        if stride and stride[-1] != 1:
             raise ValueError("innermost dimension must be contiguous")
-        return x.data_ptr()
+        return data_ptr()
     if hasattr(x, "ctypes"):
         if not x.flags["C_CONTIGUOUS"]:
             raise ValueError("array must be C-contiguous")

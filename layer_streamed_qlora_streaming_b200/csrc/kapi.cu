@@ -291,7 +291,7 @@ lst_status lst_k_policy_loss(const float* logits, int64_t T, int32_t V, const in
                      cfg->norm, cfg->adv_per_seq ? 1 : 0, logp, out, B16(dlogits), scratch};
   if (!policy_args_ok(a)) return LST_ERR_ARG;
   const cudaError_t e = policy_begin(a, S(stream));
-  return st(e != cudaSuccess ? e : policy_rows(a, 0, T, S(stream)));
+  return st(e != cudaSuccess ? e : policy_rows(a, 0, T, true, S(stream)));
 }
 
 lst_status lst_k_lora_skinny(const uint16_t* X, int64_t ldx, int64_t T, int32_t K, const uint16_t* Bop, int64_t ldb,

@@ -73,35 +73,51 @@ __device__ __forceinline__ Token policy_token(const PolicyArgs& a, float A, floa
   return {make_float4(fmaf(a.beta, kl, -(cut ? cl : in)), kl, cut ? 1.f : 0.f, r), fmaf(a.beta, dkl, cut ? 0.f : -in)};
 }
 
-// One CTA: counts the mask and leaves the weight of a counted token of each sequence.
+// One CTA: counts the mask and leaves the weight of a counted token of each sequence. A warp takes up to
+// 256 tokens of one sequence at a time, its loads independent; the counts are whole numbers, added in
+// shared memory in any order (in global memory, by one warp a sequence, where there are more sequences).
+constexpr int kSeqs = 1024;
 __global__ void __launch_bounds__(1024) k_policy_weights(const int32_t* __restrict__ mask, int64_t T, int S, int norm,
                                                          float* __restrict__ scratch) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int64_t part[32];
-  __shared__ float common;
+  __shared__ int count[kSeqs];
+  __shared__ unsigned long long total;
   float* w = seq_weight(scratch, T);
-  const int64_t nseq = T / S;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t mine = 0;
-  for (int64_t b = warp; b < nseq; b += 32) {
-    int n = 0;
-    for (int i = lane; i < S; i += 32) n += mask ? mask[b * S + i] != 0 : 1;
-    n = __reduce_add_sync(0xffffffffu, n);
-    mine += n;
-    if (lane == 0) w[b] = norm == 1 ? (n ? 1.f / ((float)nseq * (float)n) : 0.f) : 1.f / (float)T;
-  }
-  if (lane == 0) part[warp] = mine;
-  __syncthreads();
+  const int nseq = (int)(T / S), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool few = nseq <= kSeqs;
   if (threadIdx.x == 0) {
     reinterpret_cast<unsigned*>(scratch)[0] = 0;
-    int64_t n = 0;
-    for (int i = 0; i < 32; ++i) n += part[i];
-    common = n ? 1.f / (float)n : 0.f;
+    total = 0;
+  }
+  if (few)
+    for (int b = threadIdx.x; b < nseq; b += 1024) count[b] = 0;
+  __syncthreads();
+  const int step = few ? 256 : S, parts = (S + step - 1) / step;
+  for (int64_t u = warp; u < (int64_t)nseq * parts; u += 32) {
+    const int b = (int)(u / parts), i0 = (int)(u % parts) * step, i1 = min(S, i0 + step);
+    int n = 0;
+    if (mask) {
+      const int32_t* m = mask + (int64_t)b * S;
+      for (int i = i0 + lane; i < i1; i += 256) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) n += i + 32 * e < i1 && m[i + 32 * e] != 0;
+      }
+      n = __reduce_add_sync(0xffffffffu, n);
+    } else {
+      n = i1 - i0;
+    }
+    if (lane == 0) {
+      atomicAdd(&total, (unsigned long long)n);
+      if (few) atomicAdd(&count[b], n);
+      else w[b] = (float)n;
+    }
   }
   __syncthreads();
-  if (norm == 0)
-    for (int64_t b = threadIdx.x; b < nseq; b += blockDim.x) w[b] = common;
+  for (int b = threadIdx.x; b < nseq; b += 1024) {
+    const float n = few ? (float)count[b] : w[b];
+    w[b] = norm == 0 ? (total ? 1.f / (float)total : 0.f) : norm == 1 ? (n > 0.f ? 1.f / ((float)nseq * n) : 0.f) : 1.f / (float)T;
+  }
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -159,7 +175,7 @@ __device__ __forceinline__ void finish_rows(const PolicyArgs& a, int done, int n
 struct RowInfo {
   int64_t lrow;
   int y;
-  float xy, adv, old, ref, w;
+  float xy, adv, old, ref;
 };
 constexpr int kZeroBytes = 1024;
 
@@ -180,7 +196,7 @@ constexpr int kZeroBytes = 1024;
 // rows that do not count.
 template <int NV, int THREADS, int PER_SM>
 __global__ void __launch_bounds__(THREADS, PER_SM)
-k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice) {
+k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int early) {
   static_assert(NV % 2 == 0 && kZeroBytes >= 128 * 8, "two halves; the zeros' space is reused");
   extern __shared__ __align__(16) float ring[];  // three halves of a slice
   __shared__ __align__(16) uint8_t zeros[kZeroBytes];
@@ -209,7 +225,9 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice) {
   fence_proxy_async();  // the zeros are read by bulk stores
   __syncthreads();
   cluster_sync_all();  // every CTA's barriers are set up before a peer's pair can arrive
-  pdl_wait();
+  // early: the kernel in front is k_policy_weights, which lets this one start once its own predecessors
+  // have completed. All that it leaves is read by thread 0, which waits for it there.
+  if (!early) pdl_wait();
   pdl_trigger();
 
   if (warp == ncw) {  // producer
@@ -221,7 +239,7 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice) {
     };
     for (int64_t base = first; base < rows && ok; base += 32 * clusters) {
       const int64_t mine = base + lane * clusters;
-      RowInfo r{mine, 0, 0.f, 0.f, 0.f, 0.f, 0.f};
+      RowInfo r{mine, 0, 0.f, 0.f, 0.f, 0.f};
       bool live = false;
       if (mine < rows) {
         const int64_t t = row0 + mine;
@@ -236,7 +254,6 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice) {
           r.adv = a.adv[a.adv_per_seq ? t / a.S : t];
           r.old = a.old_logp ? a.old_logp[t] : 0.f;
           r.ref = a.ref_logp ? a.ref_logp[t] : 0.f;
-          r.w = seq_weight(a.scratch, a.T)[t / a.S];
         } else if (z == 0) {
           a.logp[t] = 0.f;
           reinterpret_cast<float4*>(row_terms(a.scratch))[t] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -303,6 +320,7 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice) {
     return;
   }
 
+  if (threadIdx.x == 0) pdl_wait();
   int it = 0, g = 0;  // counted rows, halves
   bool ok = true;
   for (; ok; ++it) {
@@ -318,6 +336,8 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice) {
     const int off = (int)(reinterpret_cast<uintptr_t>(x) >> 2) & 3;
     const int b = z * slice, s1 = min((a.V + off + 3) / 4, b + slice);
     const bool dvec = (reinterpret_cast<uintptr_t>(d - off) & 7) == 0;
+    float w = 0.f;  // thread 0: the row's weight
+    if (threadIdx.x == 0) w = __ldcg(seq_weight(a.scratch, a.T) + (uint32_t)t / (uint32_t)a.S);
     float v[4 * NV];
     // this thread's slots: those n < NV / 2 with n * nc < mine[0], and as many of the second half
     const int mine[2] = {min(half, s1 - b) - (int)threadIdx.x, s1 - b - half - (int)threadIdx.x};
@@ -375,11 +395,11 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice) {
         const RowInfo& r = info[it & 3];
         const float l2 = log2f(rs), logp = (fmaf(r.xy, kLog2e, -rm) - l2) * kLn2;
         const Token k = policy_token(a, r.adv, r.old, r.ref, logp);
-        factor = make_float2(rm + l2, -r.w * k.slope);
+        factor = make_float2(rm + l2, -w * k.slope);
         if (z == 0) {
           a.logp[t] = logp;
           reinterpret_cast<float4*>(row_terms(a.scratch))[t] =
-              make_float4(r.w * k.terms.x, r.w * k.terms.y, r.w * k.terms.z, r.w * k.terms.w);
+              make_float4(w * k.terms.x, w * k.terms.y, w * k.terms.z, w * k.terms.w);
         }
       }
     }
@@ -392,13 +412,13 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice) {
     for (int n = 0; n < NV; ++n) {
       const int h = n / (NV / 2), k = (n - h * (NV / 2)) * nc;
       if (k >= mine[h]) continue;
-      const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(v[4 * n] * f, v[4 * n + 1] * f),
-                                   __floats2bfloat162_rn(v[4 * n + 2] * f, v[4 * n + 3] * f)};
+      const __nv_bfloat162 g4[2] = {__floats2bfloat162_rn(v[4 * n] * f, v[4 * n + 1] * f),
+                                    __floats2bfloat162_rn(v[4 * n + 2] * f, v[4 * n + 3] * f)};
       const int c = 4 * (b + h * half + k + (int)threadIdx.x) - off;
       if (whole || (dvec && c >= 0 && c + 4 <= a.V)) {
-        *reinterpret_cast<uint2*>(d + c) = *reinterpret_cast<const uint2*>(w);
+        *reinterpret_cast<uint2*>(d + c) = *reinterpret_cast<const uint2*>(g4);
       } else {
-        const bf16* q = reinterpret_cast<const bf16*>(w);
+        const bf16* q = reinterpret_cast<const bf16*>(g4);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (c + e >= 0 && c + e < a.V) d[c + e] = q[e];
@@ -476,7 +496,8 @@ __global__ void __launch_bounds__(512) k_policy_rows(const PolicyArgs a, int64_t
 
 // As many clusters as are resident at once (they take the rows in turn), at most one a row.
 template <int NV, int THREADS, int PER_SM>
-cudaError_t launch_cluster(const PolicyArgs& a, int64_t row0, int64_t rows, int cs, int slice, cudaStream_t s) {
+cudaError_t launch_cluster(const PolicyArgs& a, int64_t row0, int64_t rows, int cs, int slice, bool early,
+                           cudaStream_t s) {
   const auto kernel = k_policy_cluster<NV, THREADS, PER_SM>;
   const int half = (slice + 1) / 2;
   const int threads = std::max(32, ((half + NV / 2 - 1) / (NV / 2) + 31) / 32 * 32) + 32, smem = 3 * half * 16;
@@ -512,7 +533,7 @@ cudaError_t launch_cluster(const PolicyArgs& a, int64_t row0, int64_t rows, int 
   }
   const int64_t clusters = std::min<int64_t>(rows, fit.clusters);
   return launch_k(kernel, dim3((unsigned)(clusters * cs)), dim3((unsigned)threads), (size_t)smem, s, (unsigned)cs, a, row0,
-                  rows, slice);
+                  rows, slice, early ? 1 : 0);
 }
 
 }  // namespace
@@ -532,7 +553,7 @@ cudaError_t policy_begin(const PolicyArgs& a, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t policy_rows(const PolicyArgs& a, int64_t row0, int64_t rows, cudaStream_t s) {
+cudaError_t policy_rows(const PolicyArgs& a, int64_t row0, int64_t rows, bool early, cudaStream_t s) {
   if (!policy_args_ok(a) || row0 < 0 || rows <= 0 || row0 + rows > a.T) return cudaErrorInvalidValue;
   // A CTA takes up to 4750 slots (224 consumers of 22, three half slices of shared memory), two CTAs an SM. A few rows are spread further, so
   // that every SM has some of them, and a shorter slice is a shorter chain for a row.
@@ -541,10 +562,10 @@ cudaError_t policy_rows(const PolicyArgs& a, int64_t row0, int64_t rows, cudaStr
   while (cs < 8 && ((slots + cs - 1) / cs > 4750 || (rows * cs < 2 * device_sm_count() && slots / cs > 1024))) cs *= 2;
   const int slice = (slots + cs - 1) / cs;
   cudaError_t e;
-  if (slice <= 512) e = launch_cluster<2, 288, 4>(a, row0, rows, cs, slice, s);
-  else if (slice <= 1536) e = launch_cluster<6, 288, 4>(a, row0, rows, cs, slice, s);
-  else if (slice <= 4750) e = launch_cluster<22, 256, 2>(a, row0, rows, cs, slice, s);
-  else if (slice <= 9400) e = launch_cluster<22, 512, 1>(a, row0, rows, cs, slice, s);
+  if (slice <= 512) e = launch_cluster<2, 288, 4>(a, row0, rows, cs, slice, early, s);
+  else if (slice <= 1536) e = launch_cluster<6, 288, 4>(a, row0, rows, cs, slice, early, s);
+  else if (slice <= 4750) e = launch_cluster<22, 256, 2>(a, row0, rows, cs, slice, early, s);
+  else if (slice <= 9400) e = launch_cluster<22, 512, 1>(a, row0, rows, cs, slice, early, s);
   else e = launch_k(k_policy_rows, dim3((unsigned)rows), dim3(512), 0, s, 0, a, row0);
   note_launch(1);
   return e != cudaSuccess ? e : cudaGetLastError();
