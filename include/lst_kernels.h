@@ -104,7 +104,7 @@ lst_status lst_k_attention_bwd(const uint16_t* q, int64_t ldq, const uint16_t* k
  * when j <= i and (i - j < window or j < sinks); window >= S is plain causal attention. Long answers
  * are sampled this way, with a cache of the last `window` tokens and the first `sinks` ones; training
  * on them has to see the same keys. Arguments as lst_k_attention_fwd (any hq a multiple of hkv), o
- * 16-byte aligned with ldo a multiple of 8; window >= 1, sinks >= 0; T * hq below 2^31. The
+ * 16-byte aligned with ldo a multiple of 8; window >= 1, sinks >= 0; T * hq below 2^31, T / S * hkv below 2^16. The
  * probabilities enter the P V product as bf16, so v has bf16's range. Rows of one sequence never
  * reach another's result; within a sequence a NaN or infinity in k or v may reach queries that share
  * a 128-row tile with its visible ones. */
@@ -116,7 +116,7 @@ lst_status lst_k_attention_window_fwd(const uint16_t* q, int64_t ldq, const uint
 /* Its backward: dq, dk, dv bf16 (16-byte aligned, row strides multiples of 8) from dout and the
  * forward's o and lse; dk and dv add the query heads of their group. scratch: fp32
  * [lst_k_attention_window_scratch(...)], 16-byte aligned, not shared by calls that may overlap on the
- * GPU; its first T * hq values come back as rowsum(dout * o). Deterministic (no atomics). */
+ * GPU. Deterministic (no atomics). */
 lst_status lst_k_attention_window_bwd(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk,
                                       const uint16_t* v, int64_t ldv, const uint16_t* o, int64_t ldo,
                                       const uint16_t* dout, int64_t lddo, const float* lse,

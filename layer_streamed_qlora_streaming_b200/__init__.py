@@ -150,7 +150,7 @@ def _ptr(x) -> int | None:
     if data_ptr is not None:
         # row-strided views are fine: every entry point takes explicit leading dimensions
         stride = x.stride()
-        if stride and stride[-1] != 1:
+        if stride and stride[-1] != 1 and x.shape[-1] > 1:
             raise ValueError("innermost dimension must be contiguous")
         return data_ptr()
     if hasattr(x, "ctypes"):

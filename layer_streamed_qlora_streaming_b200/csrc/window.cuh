@@ -10,16 +10,17 @@ struct WinArgs : AttnArgs {
   int window;  // >= 1
   int sinks;   // >= 0
 };
-struct WinBwdArgs : AttnBwdArgs {  // D: scratch of window_scratch() floats, D itself in front
+struct WinBwdArgs : AttnBwdArgs {  // D: window_scratch() floats, 16-byte aligned
   int window;
   int sinks;
 };
 
 bool window_shape_ok(int64_t T, int S, int hq, int hkv, int hd, int window, int sinks);
-// fp32 values of scratch that window_bwd needs: D [T, hq], then what its dK / dV sums are split into.
+// fp32 values of scratch that window_bwd needs: (lse, D) of every query, then what its dK / dV sums are
+// split into.
 int64_t window_scratch(int64_t T, int S, int hq, int hkv, int hd, int window, int sinks);
 
-cudaError_t window_fwd(const WinArgs& a, cudaStream_t s);
-cudaError_t window_bwd(const WinBwdArgs& a, cudaStream_t s);
+cudaError_t window_fwd(WinArgs a, cudaStream_t s);
+cudaError_t window_bwd(WinBwdArgs a, cudaStream_t s);
 
 }  // namespace lst

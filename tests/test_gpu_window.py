@@ -12,7 +12,7 @@ that of fp32.
     dP and D are fp32 sums of hd products: ed = (2 hd + 8) f max(sum |do||v|, sum |do||o|);
     dS = P (dP - D) has error P ed + e |dS| and is rounded to bf16 (u |dS|), P to bf16 in dv:
     dq: u |dq| + scale sum_j [(u (1 + u) + 2 e) |dS| + P ed] |k|, dk the same with q over (h, i);
-    dv: u |dv| + (u (1 + u) + 2 e) sum P |do|;      D: (2 hd + 8) f sum |do||o|.
+    dv: u |dv| + (u (1 + u) + 2 e) sum P |do|.
 The fp32 sums of the products over keys (at most 2 S terms of the magnitudes summed above) are below
 2 S f of them: counted in e."""
 import numpy as np
@@ -105,8 +105,6 @@ class Case:
         abs_d = (do.abs() * got_o.abs()).sum(-1, keepdim=True)
         ed = (2 * hd + 8) * F * torch.maximum((do.abs() @ v.abs().transpose(-1, -2)).masked_fill(~vis, 0).amax(-1, keepdim=True), abs_d)
         off_dS = (U * (1 + U) + 2 * e) * dS.abs() + P * ed
-        within("D", self.scratch[:self.T * self.hq].double().reshape(self.B, S, self.hq).transpose(1, 2), D[..., 0],
-               (2 * hd + 8) * F * abs_d[..., 0] + 1e-30)
         shared = lambda x: x.reshape(self.B, self.hkv, grp, S, hd).sum(2)  # noqa: E731
         dq = scale * dS @ k
         within("dq", self.heads(self.dq, self.hq), dq, U * dq.abs() + scale * off_dS @ k.abs() + 1e-30)

@@ -166,3 +166,12 @@ def test_policy_scratch_sizes():
         with pytest.raises(lst.LstError):
             lst.policy_scratch(*bad)
     assert C.sizeof(lst.Policy) == 20
+
+
+def test_pointer_of_a_one_element_tensor_with_any_stride():
+    # a dimension of one element has no stride to speak of; two strided ones are refused
+    x = torch.arange(8.0)
+    assert lst._ptr(x[::4][:1]) == x.data_ptr()
+    assert lst._ptr(x.view(4, 2)[:, :1].t()[:, :1]) == x.data_ptr()
+    with pytest.raises(ValueError):
+        lst._ptr(x[::4])
