@@ -44,6 +44,20 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t db, uin
       "r"(a), "l"(db), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The descriptor of a tile `bytes` further. Descriptors are made once a block: building two for every MMA
+// cost the issuing thread about 110 cycles each, of the 64 that an MMA of 128 x 128 x 16 takes.
+__device__ __forceinline__ uint64_t at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+// True for one lane of a converged warp, always the same one. The TMA and MMA warps run their loops with all
+// lanes and issue under this, so that no lane runs ahead while the instructions' uniform operands live.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -96,6 +110,40 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, uint32_t chunk, const CU
                                           int row, int b) {
 #pragma unroll
   for (int c = 0; c < HD / 64; ++c) tma_load_3d(dst + c * chunk, m, bar, col + c * 64, row, b);
+}
+
+// w rows of a key tile (w a multiple of 16), in one box where they are more than 32
+template <int HD>
+__device__ __forceinline__ void load_keys(uint8_t* dst, uint32_t chunk, const CUtensorMap* m, const CUtensorMap* m16,
+                                          uint64_t* bar, int col, int row, int w, int b) {
+  mbar_arrive_expect_tx(bar, (uint32_t)(w <= 32 ? w : kQB) * 2 * HD);
+  if (w <= 32) {
+    for (int r = 0; r < w; r += 16) load_tile<HD>(dst + r * 128, chunk, m16, bar, col, row + r, b);
+  } else {
+    load_tile<HD>(dst, chunk, m, bar, col, row, b);
+  }
+}
+// D = A B^T over HD columns, both K-major in chunks of 64 columns
+template <int HD>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint32_t achunk, uint64_t bb, uint32_t bchunk, uint32_t id) {
+#pragma unroll
+  for (int kk = 0; kk < HD / 16; ++kk)
+    umma_bf16(d, at(a, (kk >> 2) * achunk + (kk & 3) * 32), at(bb, (kk >> 2) * bchunk + (kk & 3) * 32), id, kk != 0);
+}
+// D (+)= A B over w <= N rows of B (MN-major, 128-byte rows): A bf16 in TMEM, 16 rows of B every 8 columns; with HALF,
+// rows [HALF, ...) of it HALF columns behind the first
+template <int N, int HALF>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bb, uint32_t id, int w, bool add) {
+  const auto step = [&](int kk, uint32_t acc) {
+    umma_ts(d, a + (HALF ? kk * 16 / HALF * HALF + kk * 16 % HALF / 2 : kk * 8), at(bb, kk * 16 * 128), id, acc);
+  };
+  if (w == N) {
+#pragma unroll
+    for (int kk = 0; kk < N / 16; ++kk) step(kk, kk > 0 || add);
+  } else {
+#pragma unroll 1
+    for (int kk = 0; kk * 16 < w; ++kk) step(kk, kk > 0 || add);
+  }
 }
 
 // ---------------------------------------------------------------------------------- forward
@@ -156,55 +204,44 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
   pdl_trigger();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       mbar_arrive_expect_tx(q_full, C::TILE);
       load_tile<HD>(sQ, C::CH, &tmQ, q_full, h * HD, q0, b);
-      for (int j = 0; j < kb.n; ++j) {
-        const int k0 = kb.k0(j), w = kb.width(j);
-        for (int kv = 0; kv < 2; ++kv) {
-          uint64_t* full = kv ? v_full : k_full;
-          if (j > 0 && !mbar_wait(kv ? v_empty : k_empty, (j - 1) & 1)) {
-            j = kb.n;
-            break;
-          }
-          uint8_t* dst = kv ? sV : sK;
-          if (w <= 32) {
-            mbar_arrive_expect_tx(full, (uint32_t)w * 2 * HD);
-            for (int r = 0; r < w; r += 16)
-              load_tile<HD>(dst + r * 128, C::CH, kv ? &tmV16 : &tmK16, full, kvh * HD, k0 + r, b);
-          } else {
-            mbar_arrive_expect_tx(full, C::TILE);
-            load_tile<HD>(dst, C::CH, kv ? &tmV : &tmK, full, kvh * HD, k0, b);
-          }
-        }
+    }
+    __syncwarp();
+    bool ok = true;
+    for (int j = 0; j < kb.n && ok; ++j) {
+      const int k0 = kb.k0(j), w = kb.width(j);
+      for (int kv = 0; kv < 2; ++kv) {
+        if (j > 0 && !(ok = warp_wait(kv ? v_empty : k_empty, (j - 1) & 1))) break;
+        if (elect_one())
+          load_keys<HD>(kv ? sV : sK, C::CH, kv ? &tmV : &tmK, kv ? &tmV16 : &tmK16, kv ? v_full : k_full, kvh * HD, k0, w, b);
+        __syncwarp();
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idO = umma_idesc_bf16(128, HD, 0, 1);
-      const uint32_t q = smem_u32(sQ), k = smem_u32(sK), v = smem_u32(sV);
-      bool ok = mbar_wait(q_full, 0);
-      for (int j = 0; j <= kb.n && ok; ++j) {
-        if (j > 0) {  // O += P_{j-1} V_{j-1}
-          if (!(ok = mbar_wait(p_full, (j - 1) & 1) && mbar_wait(v_full, (j - 1) & 1))) break;
-          tc_fence_after();
-          const int steps = kb.width(j - 1) / 16;
-          for (int kk = 0; kk < steps; ++kk)
-            umma_ts(tO, tS + kk * 8, umma_desc(v + kk * 16 * 128, C::CH, 1024), idO, (j > 1 || kk > 0) ? 1 : 0);
+    constexpr uint32_t idO = umma_idesc_bf16(128, HD, 0, 1);
+    bool ok = warp_wait(q_full, 0);
+    for (int j = 0; j <= kb.n && ok; ++j) {
+      if (j > 0) {  // O += P_{j-1} V_{j-1}
+        if (!(ok = warp_wait(p_full, (j - 1) & 1) && warp_wait(v_full, (j - 1) & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_ts<kQB, 0>(tO, tS, umma_desc(smem_u32(sV), C::CH, 1024), idO, kb.width(j - 1), j > 1);
           umma_commit(j < kb.n ? v_empty : o_full);
         }
-        if (j < kb.n) {  // S = Q K_j^T
-          if (!(ok = mbar_wait(k_full, j & 1))) break;
-          tc_fence_after();
-          const uint32_t idS = umma_idesc_bf16(128, kb.width(j), 0, 0);
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::CH + (kk & 3) * 32;
-            umma_bf16(tS, umma_desc(q + off, 16, 1024), umma_desc(k + off, 16, 1024), idS, kk != 0);
-          }
+        __syncwarp();
+      }
+      if (j < kb.n) {  // S = Q K_j^T
+        if (!(ok = warp_wait(k_full, j & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_ss<HD>(tS, umma_desc(smem_u32(sQ), 16, 1024), C::CH, umma_desc(smem_u32(sK), 16, 1024), C::CH,
+                     umma_idesc_bf16(128, kb.width(j), 0, 0));
           umma_commit(s_full);
           umma_commit(k_empty);
         }
+        __syncwarp();
       }
     }
   } else {
@@ -301,6 +338,7 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       if (live) p.lse[t * p.hq + h] = (m + log2f(l)) * kLn2;
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -367,7 +405,7 @@ struct DqCfg {
   static constexpr uint32_t CH = kQB * 128;
   static constexpr uint32_t TILE = (HD / 64) * CH;
   static constexpr int NK = 3, NV = 2;
-  static constexpr uint32_t SMEM = (2 + NK + NV) * TILE + 1024 + 256;
+  static constexpr uint32_t SMEM = (2 + NK + NV) * TILE + 1024 + 256 + kQB * 4;
 };
 
 template <int HD>
@@ -384,6 +422,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   uint64_t *k_full = bars + 6, *k_empty = k_full + C::NK, *v_full = k_empty + C::NK, *v_empty = v_full + C::NV;
   constexpr int kBars = 6 + 2 * C::NK + 2 * C::NV;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
+  float* sD = reinterpret_cast<float*>(bars + kBars + 1);  // [128]
 
   const int nq = (p.S + kQB - 1) / kQB;
   const int h = blockIdx.x % p.hq, u = blockIdx.x / p.hq;
@@ -414,72 +453,63 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   pdl_trigger();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       mbar_arrive_expect_tx(q_full, 2 * C::TILE);
       load_tile<HD>(sQ, C::CH, &tmQ, q_full, h * HD, q0, b);
       load_tile<HD>(sO, C::CH, &tmO, q_full, h * HD, q0, b);
-      bool ok = true;
-      for (int j = 0; j < kb.n && ok; ++j) {
-        const int k0 = kb.k0(j), w = kb.width(j);
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const int ns = kv ? C::NV : C::NK, s = j % ns;
-          uint64_t* full = (kv ? v_full : k_full) + s;
-          if (j >= ns && !(ok = mbar_wait((kv ? v_empty : k_empty) + s, (j / ns - 1) & 1))) break;
-          uint8_t* dst = (kv ? sV : sK) + s * C::TILE;
-          if (w <= 32) {
-            mbar_arrive_expect_tx(full, (uint32_t)w * 2 * HD);
-            for (int r = 0; r < w; r += 16)
-              load_tile<HD>(dst + r * 128, C::CH, kv ? &tmV16 : &tmK16, full, kvh * HD, k0 + r, b);
-          } else {
-            mbar_arrive_expect_tx(full, C::TILE);
-            load_tile<HD>(dst, C::CH, kv ? &tmV : &tmK, full, kvh * HD, k0, b);
-          }
-        }
+    }
+    __syncwarp();
+    bool ok = true;
+    for (int j = 0; j < kb.n && ok; ++j) {
+      const int k0 = kb.k0(j), w = kb.width(j);
+      for (int kv = 0; kv < 2; ++kv) {
+        const int ns = kv ? C::NV : C::NK, s = j % ns;
+        if (j >= ns && !(ok = warp_wait((kv ? v_empty : k_empty) + s, (j / ns - 1) & 1))) break;
+        if (elect_one())
+          load_keys<HD>((kv ? sV : sK) + s * C::TILE, C::CH, kv ? &tmV : &tmK, kv ? &tmV16 : &tmK16,
+                        (kv ? v_full : k_full) + s, kvh * HD, k0, w, b);
+        __syncwarp();
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idQ = umma_idesc_bf16(128, HD, 0, 1);
-      const uint32_t q = smem_u32(sQ), o = smem_u32(sO);
-      bool ok = mbar_wait(q_full, 0);
-      const auto scores = [&](int j) {  // S_j = Q K_j^T
-        if (!(ok = ok && mbar_wait(&k_full[j % C::NK], (j / C::NK) & 1))) return;
-        tc_fence_after();
-        const uint32_t k = smem_u32(sK + (j % C::NK) * C::TILE), id = umma_idesc_bf16(128, kb.width(j), 0, 0);
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::CH + (kk & 3) * 32;
-          umma_bf16(tmem + (j & 1) * 128, umma_desc(q + off, 16, 1024), umma_desc(k + off, 16, 1024), id, kk != 0);
-        }
+    constexpr uint32_t idQ = umma_idesc_bf16(128, HD, 0, 1);
+    bool ok = warp_wait(q_full, 0);
+    const auto scores = [&](int j) {  // S_j = Q K_j^T
+      if (!(ok = ok && warp_wait(&k_full[j % C::NK], (j / C::NK) & 1))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_ss<HD>(tmem + (j & 1) * 128, umma_desc(smem_u32(sQ), 16, 1024), C::CH,
+                   umma_desc(smem_u32(sK + j % C::NK * C::TILE), 16, 1024), C::CH, umma_idesc_bf16(128, kb.width(j), 0, 0));
         umma_commit(&s_full[j & 1]);
-      };
-      const auto dprobs = [&](int j) {  // dP_j = dO V_j^T
-        if (!(ok = ok && mbar_wait(&v_full[j % C::NV], (j / C::NV) & 1))) return;
-        tc_fence_after();
-        const uint32_t v = smem_u32(sV + (j % C::NV) * C::TILE), id = umma_idesc_bf16(128, kb.width(j), 0, 0);
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::CH + (kk & 3) * 32;
-          umma_bf16(tP, umma_desc(o + off, 16, 1024), umma_desc(v + off, 16, 1024), id, kk != 0);
-        }
+      }
+      __syncwarp();
+    };
+    const auto dprobs = [&](int j) {  // dP_j = dO V_j^T
+      if (!(ok = ok && warp_wait(&v_full[j % C::NV], (j / C::NV) & 1))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_ss<HD>(tP, umma_desc(smem_u32(sO), 16, 1024), C::CH, umma_desc(smem_u32(sV + j % C::NV * C::TILE), 16, 1024),
+                   C::CH, umma_idesc_bf16(128, kb.width(j), 0, 0));
         umma_commit(dp_full);
         umma_commit(&v_empty[j % C::NV]);
-      };
-      scores(0);
-      dprobs(0);
-      if (kb.n > 1) scores(1);
-      for (int j = 0; j < kb.n && ok; ++j) {
-        if (!(ok = mbar_wait(ds_full, j & 1))) break;  // dS_j is written, dP_j has been read
-        if (j + 1 < kb.n) dprobs(j + 1);
-        tc_fence_after();
-        const uint32_t k = smem_u32(sK + (j % C::NK) * C::TILE), ds = tmem + (j & 1) * 128;
-        const int steps = kb.width(j) / 16;
-        for (int kk = 0; kk < steps; ++kk)  // each half of the columns holds its own 64 keys' dS
-          umma_ts(tQ, ds + (kk >> 2) * 64 + (kk & 3) * 8, umma_desc(k + kk * 16 * 128, C::CH, 1024), idQ,
-                  (j | kk) != 0);
-        umma_commit(j + 1 < kb.n ? &k_empty[j % C::NK] : done);
-        if (j + 2 < kb.n) scores(j + 2);
       }
+      __syncwarp();
+    };
+    scores(0);
+    dprobs(0);
+    if (kb.n > 1) scores(1);
+    for (int j = 0; j < kb.n && ok; ++j) {
+      if (!(ok = warp_wait(ds_full, j & 1))) break;  // dS_j is written, dP_j has been read
+      if (j + 1 < kb.n) dprobs(j + 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {  // each half of a block's columns holds its own 64 keys' dS
+        mma_ts<kQB, 64>(tQ, tmem + (j & 1) * 128, umma_desc(smem_u32(sK + j % C::NK * C::TILE), C::CH, 1024), idQ,
+                        kb.width(j), j > 0);
+        umma_commit(j + 1 < kb.n ? &k_empty[j % C::NK] : done);
+      }
+      __syncwarp();
+      if (j + 2 < kb.n) scores(j + 2);
     }
   } else {
     const int half = (int)(threadIdx.x - 64) >> 7;
@@ -488,31 +518,46 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     const bool live = i < p.S;
     const int64_t t = (int64_t)b * p.S + i;
     const float sl2 = p.scale * kLog2e;
-    // D of the row, by both its threads in the same order, from the forward's unrounded o where it was kept
-    float lse2 = INFINITY, D = 0.f;
-    if (live) {
-      lse2 = p.lse[t * p.hq + h] * kLog2e;
-      const __nv_bfloat16* dp = p.dout + t * p.lddo + (int64_t)h * HD;
-      const __nv_bfloat16* op = p.o + t * p.ldo + (int64_t)h * HD;
-      const float* o32 = p.o32 ? p.o32 + (t * p.hq + h) * HD : nullptr;
-#pragma unroll 4
-      for (int c = 0; c < HD; c += 8) {
-        const uint4 du = *reinterpret_cast<const uint4*>(dp + c);
-        const __nv_bfloat16* d8 = reinterpret_cast<const __nv_bfloat16*>(&du);
-        float o8[8];
-        if (o32) {
-          *reinterpret_cast<float4*>(o8) = *reinterpret_cast<const float4*>(o32 + c);
-          *reinterpret_cast<float4*>(o8 + 4) = *reinterpret_cast<const float4*>(o32 + c + 4);
-        } else {
-          const uint4 ou = *reinterpret_cast<const uint4*>(op + c);
-          const __nv_bfloat16* b8 = reinterpret_cast<const __nv_bfloat16*>(&ou);
+    // D of the tile's rows, from the forward's unrounded o where it was kept: a warp takes 16 rows, HD / 8
+    // lanes a row, every load in flight before the first sum
+    {
+      constexpr int LPR = HD / 8, RPI = 32 / LPR;  // lanes a row, rows a load
+      const int w8 = warp - 2, col = lane % LPR * 8;
+      uint4 dv[16 / RPI];
+      float4 ov[16 / RPI][2];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o8[e] = __bfloat162float(b8[e]);
+      for (int n = 0; n < 16 / RPI; ++n) {
+        const int row = q0 + w8 * 16 + n * RPI + lane / LPR;
+        const int64_t tt = (int64_t)b * p.S + row;
+        dv[n] = make_uint4(0, 0, 0, 0);
+        ov[n][0] = ov[n][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < p.S) {
+          dv[n] = *reinterpret_cast<const uint4*>(p.dout + tt * p.lddo + (int64_t)h * HD + col);
+          if (p.o32) {
+            const float4* src = reinterpret_cast<const float4*>(p.o32 + (tt * p.hq + h) * HD + col);
+            ov[n][0] = src[0];
+            ov[n][1] = src[1];
+          } else {
+            *reinterpret_cast<uint4*>(&ov[n][0]) = *reinterpret_cast<const uint4*>(p.o + tt * p.ldo + (int64_t)h * HD + col);
+          }
         }
+      }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) D += __bfloat162float(d8[e]) * o8[e];
+      for (int n = 0; n < 16 / RPI; ++n) {
+        const __nv_bfloat16* d8 = reinterpret_cast<const __nv_bfloat16*>(&dv[n]);
+        const __nv_bfloat16* o8 = reinterpret_cast<const __nv_bfloat16*>(&ov[n][0]);
+        const float* f8 = reinterpret_cast<const float*>(&ov[n][0]);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += __bfloat162float(d8[e]) * (p.o32 ? f8[e] : __bfloat162float(o8[e]));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane % LPR == 0) sD[w8 * 16 + n * RPI + lane / LPR] = sum;
       }
     }
+    const float lse2 = live ? p.lse[t * p.hq + h] * kLog2e : INFINITY;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const float D = sD[r];
     if (half == 0) reinterpret_cast<float2*>(p.D)[stat_row(b, h, p.hq, p.S) + i] = make_float2(lse2, D);
     bool ok = true;
     // columns [64 half, 64 half + NC) of a block
@@ -557,6 +602,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       if (live) store_grad<HD>(p.dq + t * p.lddq + (int64_t)h * HD, lo, hi, p, i, half);
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -652,14 +698,19 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   pdl_wait();
   pdl_trigger();
 
-  if (warp == 0) {
-    if (lane == 0 && n > 0) {
+  if (n <= 0) {
+    // nothing of the work fell to this part
+  } else if (warp == 0) {
+    if (elect_one()) {
       mbar_arrive_expect_tx(kv_full, 2 * C::KT);
       load_tile<HD>(sK, C::CH, &tmK, kv_full, kvh * HD, k0, b);
       load_tile<HD>(sV, C::CH, &tmV, kv_full, kvh * HD, k0, b);
-      for (int j = 0; j < n; ++j) {
-        const int s = j % C::NS, h = head(j), q = query(j);
-        if (j >= C::NS && !mbar_wait(&q_empty[s], (j / C::NS - 1) & 1)) break;
+    }
+    __syncwarp();
+    for (int j = 0; j < n; ++j) {
+      const int s = j % C::NS, h = head(j), q = query(j);
+      if (j >= C::NS && !warp_wait(&q_empty[s], (j / C::NS - 1) & 1)) break;
+      if (elect_one()) {
         uint8_t* st = sQ + s * C::STEP;
         mbar_arrive_expect_tx(&q_full[s], C::STAGE);
         load_tile<HD>(st, C::QCH, &tmQ, &q_full[s], h * HD, q, b);
@@ -667,40 +718,35 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         bulk_load(st + 2 * C::QT, reinterpret_cast<const float2*>(p.D) + stat_row(b, h, p.hq, p.S) + q, C::QB * 8,
                   &q_full[s]);
       }
+      __syncwarp();
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t idS = umma_idesc_bf16(128, C::QB, 0, 0), idG = umma_idesc_bf16(128, HD, 0, 1);
-      const uint32_t k = smem_u32(sK), v = smem_u32(sV);
-      bool ok = mbar_wait(kv_full, 0);
-      for (int j = 0; j < n + 2 && ok; ++j) {
-        if (j >= 2) {  // dV += P^T dO, dK += dS^T Q of block j - 2
-          const int i = j - 2, st = i & 1;
-          if (!(ok = mbar_wait(&t_full[st], (i >> 1) & 1))) break;
-          tc_fence_after();
-          const uint32_t q = smem_u32(sQ + (i % C::NS) * C::STEP), o = q + C::QT;
-          // the second half of the queries lies 32 columns further
-#pragma unroll
-          for (int kk = 0; kk < C::QB / 16; ++kk) {
-            const uint32_t a = st * 64 + (kk >> 1) * 32 + (kk & 1) * 8;
-            umma_ts(tV, tmem + a, umma_desc(o + kk * 16 * 128, C::QCH, 1024), idG, (i | kk) != 0);
-            umma_ts(tK, tmem + 128 + a, umma_desc(q + kk * 16 * 128, C::QCH, 1024), idG, (i | kk) != 0);
-          }
+    constexpr uint32_t idS = umma_idesc_bf16(128, C::QB, 0, 0), idG = umma_idesc_bf16(128, HD, 0, 1);
+    bool ok = warp_wait(kv_full, 0);
+    for (int j = 0; j < n + 2 && ok; ++j) {
+      if (j >= 2) {  // dV += P^T dO, dK += dS^T Q of block j - 2
+        const int i = j - 2, st = i & 1;
+        if (!(ok = warp_wait(&t_full[st], (i >> 1) & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {  // the second half of the queries lies 32 columns further
+          const uint64_t q = umma_desc(smem_u32(sQ + i % C::NS * C::STEP), C::QCH, 1024);
+          mma_ts<C::QB, 32>(tV, tmem + st * 64, at(q, C::QT), idG, C::QB, i > 0);
+          mma_ts<C::QB, 32>(tK, tmem + 128 + st * 64, q, idG, C::QB, i > 0);
           umma_commit(i + 1 < n ? &q_empty[i % C::NS] : done);
         }
-        if (j < n) {  // S^T_j = K Q_j^T, dP^T_j = V dO_j^T
-          const int st = j & 1;
-          if (!(ok = mbar_wait(&q_full[j % C::NS], (j / C::NS) & 1))) break;
-          tc_fence_after();
-          const uint32_t q = smem_u32(sQ + (j % C::NS) * C::STEP), o = q + C::QT;
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t offk = (kk >> 2) * C::CH + (kk & 3) * 32, offq = (kk >> 2) * C::QCH + (kk & 3) * 32;
-            umma_bf16(tmem + st * 64, umma_desc(k + offk, 16, 1024), umma_desc(q + offq, 16, 1024), idS, kk != 0);
-            umma_bf16(tmem + 128 + st * 64, umma_desc(v + offk, 16, 1024), umma_desc(o + offq, 16, 1024), idS, kk != 0);
-          }
+        __syncwarp();
+      }
+      if (j < n) {  // S^T_j = K Q_j^T, dP^T_j = V dO_j^T
+        const int st = j & 1;
+        if (!(ok = warp_wait(&q_full[j % C::NS], (j / C::NS) & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t q = umma_desc(smem_u32(sQ + j % C::NS * C::STEP), 16, 1024);
+          mma_ss<HD>(tmem + st * 64, umma_desc(smem_u32(sK), 16, 1024), C::CH, q, C::QCH, idS);
+          mma_ss<HD>(tmem + 128 + st * 64, umma_desc(smem_u32(sV), 16, 1024), C::CH, at(q, C::QT), C::QCH, idS);
           umma_commit(&s_full[st]);
         }
+        __syncwarp();
       }
     }
   } else {
@@ -740,7 +786,7 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       tc_fence_before();
       mbar_arrive(&t_full[st]);
     }
-    if (ok && n > 0 && warp_wait(done, 0)) {
+    if (ok && warp_wait(done, 0)) {
       tc_fence_after();
       if (np == 1) {
         const bool live = key < p.S;
@@ -774,6 +820,7 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
