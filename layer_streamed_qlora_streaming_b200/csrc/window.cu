@@ -29,7 +29,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // gemm.cu
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kQB = 128;  // rows of a query tile (the TMEM lanes), and of a key tile
+constexpr int kQB = 128;  // rows of a tile in TMEM: queries (forward, dQ) or keys (dK, dV)
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -80,24 +80,33 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 __host__ __device__ __forceinline__ int up(int a, int b) { return (a + b - 1) / b * b; }
 
 // The key blocks that the queries [q0, q0 + 128) of a sequence see, in order: sinks in front of the
-// window's first block, then the window's blocks. A block starts at a multiple of 128; its width is a
+// window's first block, then the window's blocks. A block starts at a multiple of KB; its width is a
 // multiple of 16 that covers its last visible key.
+template <int kKB>
 struct Blocks {
   int nsink, n, jb0, front, end;
   __device__ __forceinline__ Blocks(int q0, int S, int window, int sinks) {
-    const int w0 = max(0, q0 - window + 1);
-    jb0 = w0 / kQB;
-    front = min(sinks, jb0 * kQB);  // sinks that the window's blocks do not hold
-    nsink = (front + kQB - 1) / kQB;
+    jb0 = max(0, q0 - window + 1) / kKB;
+    front = min(sinks, jb0 * kKB);  // sinks that the window's blocks do not hold
+    nsink = (front + kKB - 1) / kKB;
     end = min(S, q0 + kQB);
-    n = nsink + (end + kQB - 1) / kQB - jb0;
+    n = nsink + (end + kKB - 1) / kKB - jb0;
   }
-  __device__ __forceinline__ int k0(int j) const { return (j < nsink ? j : jb0 + j - nsink) * kQB; }
+  __device__ __forceinline__ int k0(int j) const { return (j < nsink ? j : jb0 + j - nsink) * kKB; }
   __device__ __forceinline__ int width(int j) const {
     const int left = (j < nsink ? front : end) - k0(j);
-    return left >= kQB ? kQB : up(left, 16);
+    return left >= kKB ? kKB : up(left, 16);
   }
 };
+__device__ __forceinline__ uint64_t bits_below(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+// Bit c: query i sees key k0 + c, c < 64.
+__device__ __forceinline__ uint64_t visible_keys(int i, int k0, int window, int sinks) {
+  return bits_below(i - k0 + 1) & (~bits_below(i - window + 1 - k0) | bits_below(sinks - k0));
+}
+// Bit c: key j is seen by query q0 + c, c < 64.
+__device__ __forceinline__ uint64_t visible_queries(int j, int q0, int window, int sinks) {
+  return ~bits_below(j - q0) & (j < sinks ? ~0ull : bits_below(j + window - q0));
+}
 // every pair of queries [q0, q0 + nq) and keys [k0, k0 + nk) is visible
 __device__ __forceinline__ bool all_visible(int q0, int nq, int k0, int nk, int window, int sinks) {
   return k0 + nk - 1 <= q0 && (q0 + nq - 1 - k0 < window || k0 + nk <= sinks);
@@ -112,16 +121,38 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, uint32_t chunk, const CU
   for (int c = 0; c < HD / 64; ++c) tma_load_3d(dst + c * chunk, m, bar, col + c * 64, row, b);
 }
 
-// w rows of a key tile (w a multiple of 16), in one box where they are more than 32
-template <int HD>
+// w rows of a key tile (w a multiple of 16), in one box of KB rows where they are more than 32
+template <int HD, int KB>
 __device__ __forceinline__ void load_keys(uint8_t* dst, uint32_t chunk, const CUtensorMap* m, const CUtensorMap* m16,
                                           uint64_t* bar, int col, int row, int w, int b) {
-  mbar_arrive_expect_tx(bar, (uint32_t)(w <= 32 ? w : kQB) * 2 * HD);
+  mbar_arrive_expect_tx(bar, (uint32_t)(w <= 32 ? w : KB) * 2 * HD);
   if (w <= 32) {
     for (int r = 0; r < w; r += 16) load_tile<HD>(dst + r * 128, chunk, m16, bar, col, row + r, b);
   } else {
     load_tile<HD>(dst, chunk, m, bar, col, row, b);
   }
+}
+// A bf16 row (32 packed words of 64 columns) into its place of a swizzled [rows x 64] tile
+__device__ __forceinline__ void stage_row(uint8_t* tile, int row, const uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(tile + row * 128 + ((i ^ (row & 7)) * 16)) =
+        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+// D = A B^T over HD columns, A in TMEM (HD / 2 columns), B K-major in chunks of 64 columns
+template <int HD>
+__device__ __forceinline__ void mma_tt(uint32_t d, uint32_t a, uint64_t bb, uint32_t bchunk, uint32_t id) {
+#pragma unroll
+  for (int kk = 0; kk < HD / 16; ++kk) umma_ts(d, a + kk * 8, at(bb, (kk >> 2) * bchunk + (kk & 3) * 32), id, kk != 0);
 }
 // D = A B^T over HD columns, both K-major in chunks of 64 columns
 template <int HD>
@@ -147,50 +178,52 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bb, uint
 }
 
 // ---------------------------------------------------------------------------------- forward
-// One CTA per query tile of one head, two CTAs an SM: a tile's chain S -> softmax -> P V is serial, so
-// the tensor cores work on one CTA's products while the other's softmax runs, and a CTA's start and
-// end hide behind the other's blocks. 192 threads: warp 0 TMA (one K and one V tile: K j+1 arrives
-// under softmax j, V j+1 under softmax j+1), warp 1 issues the MMAs, warps 2-5 one thread a query row.
-//   S = Q K^T into TMEM; P = 2^(S' - m) as bf16 over S itself, the A operand of O += P V.
-// The reference m of a row moves only when a block's maximum exceeds it by 2^8, with O rescaled in
-// TMEM then: S of block j has completed, so have the products issued before it, P V of j - 1 among
-// them. Blocks of up to 32 keys (the usual few sinks) run a short form.
+// One CTA per query tile of one head, two CTAs an SM, so that a CTA's start and end hide behind the
+// other's blocks. 192 threads: warp 0 TMA (two K and two V blocks of 64 keys in flight), warp 1 issues
+// the MMAs, warps 2-5 one thread a query row.
+//   S = Q K^T into one of two TMEM buffers; P = 2^(S' - m) as bf16 over S itself, the A operand of O += P V.
+// While a row's thread works on block j, the tensor cores form P V of j - 1 and S of j + 1.
+// The reference m of a row moves only when a block's maximum exceeds it by 2^8; O is then rescaled in
+// TMEM, once P V of j - 1 has been added. The tile of O leaves through Q's shared memory by TMA.
 template <int HD>
 struct FwdCfg {
-  static constexpr uint32_t CH = kQB * 128;  // [128 rows x 64] bf16
-  static constexpr uint32_t TILE = (HD / 64) * CH;
-  static constexpr uint32_t SMEM = 3 * TILE + 1024 + 128;
+  static constexpr int KB = 64;  // keys of a block
+  static constexpr uint32_t CH = kQB * 128, KCH = KB * 128;  // [128 x 64], [64 x 64] bf16
+  static constexpr uint32_t TILE = (HD / 64) * CH, KT = (HD / 64) * KCH;
+  static constexpr uint32_t SMEM = TILE + 4 * KT + 1024 + 256;
 };
 
 template <int HD>
 __global__ void __launch_bounds__(192, 2)
 k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmK16,
-             const __grid_constant__ CUtensorMap tmV16, const WinArgs p) {
+             const __grid_constant__ CUtensorMap tmV16, const __grid_constant__ CUtensorMap tmO, const WinArgs p) {
   using C = FwdCfg<HD>;
+  constexpr int kKB = C::KB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sQ = smem, *sK = smem + C::TILE, *sV = smem + 2 * C::TILE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 3 * C::TILE);
-  uint64_t *q_full = bars, *k_full = bars + 1, *v_full = bars + 2, *k_empty = bars + 3, *v_empty = bars + 4,
-           *s_full = bars + 5, *p_full = bars + 6, *o_full = bars + 7;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
+  uint8_t *sQ = smem, *sK = smem + C::TILE, *sV = sK + 2 * C::KT;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + 2 * C::KT);
+  uint64_t *q_full = bars, *o_full = bars + 1, *k_full = bars + 2, *v_full = bars + 4, *k_empty = bars + 6,
+           *v_empty = bars + 8, *s_full = bars + 10, *p_full = bars + 12;  // [2] from k_full on
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
 
   const int nq = (p.S + kQB - 1) / kQB;
   const int h = blockIdx.x % p.hq, u = blockIdx.x / p.hq;
   const int b = u / nq, q0 = (nq - 1 - u % nq) * kQB;
   const int kvh = h / (p.hq / p.hkv);
-  const Blocks kb(q0, p.S, p.window, p.sinks);
+  const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 8; ++i) mbar_init(bars + i, bars + i == p_full ? 128 : 1);
+    for (int i = 0; i < 14; ++i) mbar_init(bars + i, i >= 12 ? 128 : 1);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmO);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 256);
@@ -211,38 +244,42 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     __syncwarp();
     bool ok = true;
     for (int j = 0; j < kb.n && ok; ++j) {
-      const int k0 = kb.k0(j), w = kb.width(j);
+      const int k0 = kb.k0(j), w = kb.width(j), s = j & 1;
       for (int kv = 0; kv < 2; ++kv) {
-        if (j > 0 && !(ok = warp_wait(kv ? v_empty : k_empty, (j - 1) & 1))) break;
+        if (j >= 2 && !(ok = warp_wait((kv ? v_empty : k_empty) + s, ((j >> 1) - 1) & 1))) break;
         if (elect_one())
-          load_keys<HD>(kv ? sV : sK, C::CH, kv ? &tmV : &tmK, kv ? &tmV16 : &tmK16, kv ? v_full : k_full, kvh * HD, k0, w, b);
+          load_keys<HD, kKB>((kv ? sV : sK) + s * C::KT, C::KCH, kv ? &tmV : &tmK, kv ? &tmV16 : &tmK16,
+                        (kv ? v_full : k_full) + s, kvh * HD, k0, w, b);
         __syncwarp();
       }
     }
   } else if (warp == 1) {
     constexpr uint32_t idO = umma_idesc_bf16(128, HD, 0, 1);
     bool ok = warp_wait(q_full, 0);
-    for (int j = 0; j <= kb.n && ok; ++j) {
-      if (j > 0) {  // O += P_{j-1} V_{j-1}
-        if (!(ok = warp_wait(p_full, (j - 1) & 1) && warp_wait(v_full, (j - 1) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          mma_ts<kQB, 0>(tO, tS, umma_desc(smem_u32(sV), C::CH, 1024), idO, kb.width(j - 1), j > 1);
-          umma_commit(j < kb.n ? v_empty : o_full);
-        }
-        __syncwarp();
+    const auto scores = [&](int j) {  // S_j = Q K_j^T
+      const int s = j & 1;
+      if (!(ok = ok && warp_wait(k_full + s, (j >> 1) & 1))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_ss<HD>(tS + s * kKB, umma_desc(smem_u32(sQ), 16, 1024), C::CH, umma_desc(smem_u32(sK + s * C::KT), 16, 1024),
+                   C::KCH, umma_idesc_bf16(128, kb.width(j), 0, 0));
+        umma_commit(s_full + s);
+        umma_commit(k_empty + s);
       }
-      if (j < kb.n) {  // S = Q K_j^T
-        if (!(ok = warp_wait(k_full, j & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          mma_ss<HD>(tS, umma_desc(smem_u32(sQ), 16, 1024), C::CH, umma_desc(smem_u32(sK), 16, 1024), C::CH,
-                     umma_idesc_bf16(128, kb.width(j), 0, 0));
-          umma_commit(s_full);
-          umma_commit(k_empty);
-        }
-        __syncwarp();
+      __syncwarp();
+    };
+    scores(0);
+    if (kb.n > 1) scores(1);
+    for (int j = 0; j < kb.n && ok; ++j) {
+      const int s = j & 1;
+      if (!(ok = warp_wait(v_full + s, (j >> 1) & 1) && warp_wait(p_full + s, (j >> 1) & 1))) break;
+      tc_fence_after();
+      if (elect_one()) {  // O += P_j V_j
+        mma_ts<kKB, 0>(tO, tS + s * kKB, umma_desc(smem_u32(sV + s * C::KT), C::KCH, 1024), idO, kb.width(j), j > 0);
+        umma_commit(j + 1 < kb.n ? v_empty + s : o_full);
       }
+      __syncwarp();
+      if (j + 2 < kb.n) scores(j + 2);
     }
   } else {
     const int r = (warp & 3) * 32 + lane, i = q0 + r;
@@ -250,18 +287,20 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     const float sl2 = p.scale * kLog2e;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    // one block of NC columns (those from `cols` on are not visible to any row)
+    // the first NC columns of a block
     const auto block = [&](auto nc, bool masked, int k0, int j) {
       constexpr int NC = decltype(nc)::value;
+      const uint32_t tX = tS + (j & 1) * kKB + lanes;
       float x[NC];
 #pragma unroll
-      for (int c = 0; c < NC; c += 32) tmem_ld32(tS + lanes + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
+      for (int c = 0; c < NC; c += 32) tmem_ld32(tX + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
       tmem_ld_wait();
-      if (masked) {  // visible: [i - window + 1, i] and [0, sinks), both up to i, as columns
-        const int hi = i - k0, lo = hi - p.window, sc = p.sinks - k0;
+      if (masked) {
+        const uint64_t vis = visible_keys(i, k0, p.window, p.sinks);
+        const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-          if (c > hi || (c <= lo && c >= sc)) x[c] = -INFINITY;
+          if (!(bits[c / 32] >> (c % 32) & 1)) x[c] = -INFINITY;
       }
       float pm[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -274,6 +313,8 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         l *= corr;
       }
       if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+        if (!(ok = warp_wait(v_empty + ((j - 1) & 1), ((j - 1) >> 1) & 1))) return;  // P V of j - 1 has been added
+        tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           uint32_t o[32];
@@ -286,56 +327,59 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       }
       const float mm = m > -INFINITY ? m : 0.f;  // a row that sees nothing so far
       float ps[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        x[c] = ex2_approx(fmaf(x[c], sl2, -mm));
-        ps[c & 3] += x[c];
-      }
-      l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
       uint32_t w[NC / 2];
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) w[c] = pack2(x[2 * c], x[2 * c + 1]);
+      for (int c = 0; c < NC; c += 2) {
+        const float a0 = ex2_approx(fmaf(x[c], sl2, -mm)), a1 = ex2_approx(fmaf(x[c + 1], sl2, -mm));
+        ps[c & 3] += a0;
+        ps[(c + 1) & 3] += a1;
+        w[c / 2] = pack2(a0, a1);
+      }
+      l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
 #pragma unroll
-      for (int c = 0; c < NC / 2; c += 16) tmem_st16(tS + lanes + c, w + c);
+      for (int c = 0; c < NC / 2; c += 16) tmem_st16(tX + c, w + c);
       tmem_st_wait();
     };
-    for (int j = 0; j < kb.n; ++j) {
-      if (!(ok = warp_wait(s_full, j & 1))) break;
+    for (int j = 0; j < kb.n && ok; ++j) {
+      if (!(ok = warp_wait(s_full + (j & 1), (j >> 1) & 1))) break;
       tc_fence_after();
-      const int k0 = kb.k0(j), w = kb.width(j);
-      const bool masked = !all_visible(q0, kQB, k0, kQB, p.window, p.sinks);
-      if (w <= 32) block(std::integral_constant<int, 32>{}, true, k0, j);
-      else block(std::integral_constant<int, 128>{}, masked, k0, j);
+      const int k0 = kb.k0(j);
+      if (kb.width(j) <= 32) block(std::integral_constant<int, 32>{}, true, k0, j);
+      else block(std::integral_constant<int, kKB>{}, !all_visible(q0, kQB, k0, kKB, p.window, p.sinks), k0, j);
       tc_fence_before();
-      mbar_arrive(p_full);
+      mbar_arrive(p_full + (j & 1));
     }
-    if (ok && warp_wait(o_full, 0)) {
+    ok = ok && warp_wait(o_full, 0);
+    if (ok) {
       tc_fence_after();
       const float inv = 1.f / l;
       const int64_t t = (int64_t)b * p.S + i;
-      const bool live = i < p.S;
+      if (i < p.S) p.lse[t * p.hq + h] = (m + log2f(l)) * kLn2;
 #pragma unroll 1
-      for (int c = 0; c < HD; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(tO + lanes + c, o);
+      for (int c = 0; c < HD; c += 64) {
+        float y[64];
+        uint32_t w[32];
+        tmem_ld32(tO + lanes + c, *reinterpret_cast<uint32_t(*)[32]>(y));
+        tmem_ld32(tO + lanes + c + 32, *reinterpret_cast<uint32_t(*)[32]>(y + 32));
         tmem_ld_wait();
-        if (live) {
-          float y[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv;
-          __nv_bfloat16* dst = p.o + t * p.ldo + (int64_t)h * HD + c;
+        for (int e = 0; e < 64; ++e) y[e] *= inv;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(dst + e) = make_uint4(pack2(y[e], y[e + 1]), pack2(y[e + 2], y[e + 3]),
-                                                            pack2(y[e + 4], y[e + 5]), pack2(y[e + 6], y[e + 7]));
-          if (p.o32) {
-            float* d32 = p.o32 + (t * p.hq + h) * HD + c;
+        for (int e = 0; e < 32; ++e) w[e] = pack2(y[2 * e], y[2 * e + 1]);
+        stage_row(sQ + c / 64 * C::CH, r, w);
+        if (p.o32 && i < p.S) {
+          float* d32 = p.o32 + (t * p.hq + h) * HD + c;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(d32 + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-          }
+          for (int e = 0; e < 64; e += 4) *reinterpret_cast<float4*>(d32 + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
         }
       }
-      if (live) p.lse[t * p.hq + h] = (m + log2f(l)) * kLn2;
+      fence_proxy_async();
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (warp == 2 && ok && elect_one()) {
+#pragma unroll
+      for (int c = 0; c < HD / 64; ++c) tma_store_3d(&tmO, sQ + c * C::CH, h * HD + c * 64, q0, b);
+      tma_store_wait();
     }
   }
   __syncwarp();
@@ -348,11 +392,13 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 }
 
 // Columns [part HD / 4, part HD / 4 + HD / 4) of a gradient row and their rotary partners HD / 2 further, part
-// 0 or 1: x * scale with the rotary embedding of position pos undone.
+// 0 or 1: x * scale with the rotary embedding of position pos undone, as bf16 into the row's place of a
+// swizzled tile (chunks of 64 columns).
 template <int HD>
-__device__ __forceinline__ void store_grad(__nv_bfloat16* dst, const float (&lo)[HD / 4], const float (&hi)[HD / 4],
-                                           const AttnBwdArgs& p, int pos, int part) {
+__device__ __forceinline__ void stage_grad(uint8_t* tile, uint32_t chunk, int row, const float (&lo)[HD / 4],
+                                           const float (&hi)[HD / 4], const AttnBwdArgs& p, int pos, int part) {
   constexpr int HALF = HD / 2, Q4 = HD / 4;
+  const bool rope = p.rope_cos && pos < p.S;
 #pragma unroll
   for (int c0 = 0; c0 < Q4; c0 += 8) {
     const int c = part * Q4 + c0;
@@ -361,16 +407,19 @@ __device__ __forceinline__ void store_grad(__nv_bfloat16* dst, const float (&lo)
     for (int e = 0; e < 8; ++e) {
       y1[e] = lo[c0 + e] * p.scale;
       y2[e] = hi[c0 + e] * p.scale;
-      if (p.rope_cos) {
+      if (rope) {
         const float cs = p.rope_cos[(int64_t)pos * HALF + c + e], sn = p.rope_sin[(int64_t)pos * HALF + c + e];
         const float a = y1[e] * cs + y2[e] * sn;
         y2[e] = y2[e] * cs - y1[e] * sn;
         y1[e] = a;
       }
     }
-    *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack2(y1[0], y1[1]), pack2(y1[2], y1[3]), pack2(y1[4], y1[5]), pack2(y1[6], y1[7]));
-    *reinterpret_cast<uint4*>(dst + c + HALF) =
-        make_uint4(pack2(y2[0], y2[1]), pack2(y2[2], y2[3]), pack2(y2[4], y2[5]), pack2(y2[6], y2[7]));
+    const auto put = [&](int col, const float* y) {
+      *reinterpret_cast<uint4*>(tile + col / 64 * chunk + row * 128 + ((col % 64 / 8) ^ (row & 7)) * 16) =
+          make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+    };
+    put(c, y1);
+    put(c + HALF, y2);
   }
 }
 // N consecutive TMEM columns of this thread's row
@@ -392,16 +441,23 @@ __device__ __forceinline__ void tmem_row(float (&x)[N], uint32_t addr) {
 }
 
 // What the dK / dV kernel reads of a query: its lse in units of log2 (infinity behind the sequence, which
-// makes its P zero) and D. [B, hq, S rounded up to 128], in front of the scratch.
-__host__ __device__ __forceinline__ int64_t stat_row(int b, int h, int hq, int S) { return ((int64_t)b * hq + h) * up(S, kQB); }
+// makes its P zero) and D. Two rows of S rounded up to 128 for each sequence and head, in front of the scratch.
+__host__ __device__ __forceinline__ int64_t stat_row(int b, int h, int hq, int S) {
+  return ((int64_t)b * hq + h) * 2 * up(S, kQB);
+}
 
 // ---------------------------------------------------------------------------------- dQ
-// One CTA per query tile of one head, 320 threads: warp 0 TMA (Q and dO once, three K and two V tiles
-// in flight), warp 1 the MMAs, warps 2-9 two threads a query row (half the columns of a block each).
-// S has two TMEM buffers: while the threads turn S, dP of block j into dS (bf16, over their own columns
-// of S j), the tensor cores form dQ += dS K of j - 1, S of j + 1 and dP of j + 1.
+// One CTA per query tile of one head, 320 threads: warp 0 TMA (three K and two V blocks of 128 keys in
+// flight), warp 1 the MMAs, warps 2-9 two threads a query row (half of a block's columns each).
+// Q and dO are copied into TMEM first and serve as the A operands from there: read from shared memory for
+// every block they took its whole bandwidth (128 bytes a clock: with K, V, their loads and dS K 1800
+// clocks a block, where the tensor cores take 1540). S of block j + 1 is issued as soon as the threads
+// have read S of j; dS goes over dP (bf16, the A operand of dQ += dS K), and dP of j + 1 follows that
+// product, under the exponentials of j + 1. (Blocks of 64 keys with two buffers of each took 2060 clocks
+// a block: at N = 64 the issue of an MMA takes longer than its 32 clocks.)
 template <int HD>
 struct DqCfg {
+  static constexpr int KB = 128;  // keys of a block
   static constexpr uint32_t CH = kQB * 128;
   static constexpr uint32_t TILE = (HD / 64) * CH;
   static constexpr int NK = 3, NV = 2;
@@ -412,15 +468,18 @@ template <int HD>
 __global__ void __launch_bounds__(320, 1)
 k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
             const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-            const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16, const WinBwdArgs p) {
+            const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16,
+            const __grid_constant__ CUtensorMap tmDq, const WinBwdArgs p) {
   using C = DqCfg<HD>;
+  constexpr int NK = C::NK, NV = C::NV, kKB = C::KB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sQ = smem, *sO = smem + C::TILE, *sK = smem + 2 * C::TILE, *sV = sK + C::NK * C::TILE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + C::NV * C::TILE);
-  uint64_t *q_full = bars, *dp_full = bars + 1, *ds_full = bars + 2, *done = bars + 3, *s_full = bars + 4;  // [2]
-  uint64_t *k_full = bars + 6, *k_empty = k_full + C::NK, *v_full = k_empty + C::NK, *v_empty = v_full + C::NV;
-  constexpr int kBars = 6 + 2 * C::NK + 2 * C::NV;
+  uint8_t *sQ = smem, *sO = smem + C::TILE, *sK = smem + 2 * C::TILE, *sV = sK + NK * C::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + NV * C::TILE);
+  uint64_t *a_full = bars, *s_free = bars + 1, *ds_full = bars + 2;  // of all 256 row threads
+  uint64_t *q_full = bars + 3, *s_full = bars + 4, *dp_full = bars + 5, *done = bars + 6;
+  uint64_t *k_full = bars + 7, *k_empty = k_full + NK, *v_full = k_empty + NK, *v_empty = v_full + NV;
+  constexpr int kBars = 7 + 2 * NK + 2 * NV;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   float* sD = reinterpret_cast<float*>(bars + kBars + 1);  // [128]
 
@@ -428,11 +487,11 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   const int h = blockIdx.x % p.hq, u = blockIdx.x / p.hq;
   const int b = u / nq, q0 = (nq - 1 - u % nq) * kQB;
   const int kvh = h / (p.hq / p.hkv);
-  const Blocks kb(q0, p.S, p.window, p.sinks);
+  const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kBars; ++i) mbar_init(bars + i, bars + i == ds_full ? 256 : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(bars + i, i < 3 ? 256 : 1);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -440,6 +499,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     tma_prefetch_desc(&tmO);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmDq);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -448,7 +508,8 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot, tP = tmem + 256, tQ = tmem + 384;  // S in columns 0 and 128
+  // Q and dO (64 columns each), S, dP, dQ
+  const uint32_t tmem = *tmem_slot, tA = tmem, tS = tmem + 128, tP = tmem + 256, tQ = tmem + 384;
   pdl_wait();
   pdl_trigger();
 
@@ -463,61 +524,63 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     for (int j = 0; j < kb.n && ok; ++j) {
       const int k0 = kb.k0(j), w = kb.width(j);
       for (int kv = 0; kv < 2; ++kv) {
-        const int ns = kv ? C::NV : C::NK, s = j % ns;
+        const int ns = kv ? NV : NK, s = j % ns;
         if (j >= ns && !(ok = warp_wait((kv ? v_empty : k_empty) + s, (j / ns - 1) & 1))) break;
         if (elect_one())
-          load_keys<HD>((kv ? sV : sK) + s * C::TILE, C::CH, kv ? &tmV : &tmK, kv ? &tmV16 : &tmK16,
-                        (kv ? v_full : k_full) + s, kvh * HD, k0, w, b);
+          load_keys<HD, kKB>((kv ? sV : sK) + s * C::TILE, C::CH, kv ? &tmV : &tmK, kv ? &tmV16 : &tmK16,
+                             (kv ? v_full : k_full) + s, kvh * HD, k0, w, b);
         __syncwarp();
       }
     }
   } else if (warp == 1) {
     constexpr uint32_t idQ = umma_idesc_bf16(128, HD, 0, 1);
-    bool ok = warp_wait(q_full, 0);
+    bool ok = warp_wait(a_full, 0);
     const auto scores = [&](int j) {  // S_j = Q K_j^T
-      if (!(ok = ok && warp_wait(&k_full[j % C::NK], (j / C::NK) & 1))) return;
+      const int s = j % NK;
+      if (!(ok = ok && warp_wait(k_full + s, (j / NK) & 1))) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_ss<HD>(tmem + (j & 1) * 128, umma_desc(smem_u32(sQ), 16, 1024), C::CH,
-                   umma_desc(smem_u32(sK + j % C::NK * C::TILE), 16, 1024), C::CH, umma_idesc_bf16(128, kb.width(j), 0, 0));
-        umma_commit(&s_full[j & 1]);
+        mma_tt<HD>(tS, tA, umma_desc(smem_u32(sK + s * C::TILE), 16, 1024), C::CH, umma_idesc_bf16(128, kb.width(j), 0, 0));
+        umma_commit(s_full);
       }
       __syncwarp();
     };
     const auto dprobs = [&](int j) {  // dP_j = dO V_j^T
-      if (!(ok = ok && warp_wait(&v_full[j % C::NV], (j / C::NV) & 1))) return;
+      const int s = j % NV;
+      if (!(ok = ok && warp_wait(v_full + s, (j / NV) & 1))) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_ss<HD>(tP, umma_desc(smem_u32(sO), 16, 1024), C::CH, umma_desc(smem_u32(sV + j % C::NV * C::TILE), 16, 1024),
-                   C::CH, umma_idesc_bf16(128, kb.width(j), 0, 0));
+        mma_tt<HD>(tP, tA + 64, umma_desc(smem_u32(sV + s * C::TILE), 16, 1024), C::CH,
+                   umma_idesc_bf16(128, kb.width(j), 0, 0));
         umma_commit(dp_full);
-        umma_commit(&v_empty[j % C::NV]);
+        umma_commit(v_empty + s);
       }
       __syncwarp();
     };
     scores(0);
     dprobs(0);
-    if (kb.n > 1) scores(1);
     for (int j = 0; j < kb.n && ok; ++j) {
-      if (!(ok = warp_wait(ds_full, j & 1))) break;  // dS_j is written, dP_j has been read
-      if (j + 1 < kb.n) dprobs(j + 1);
-      if (!ok) break;
+      if (j + 1 < kb.n) {
+        if (!(ok = warp_wait(s_free, j & 1))) break;
+        scores(j + 1);
+      }
+      if (!(ok = ok && warp_wait(ds_full, j & 1))) break;
       tc_fence_after();
       if (elect_one()) {  // each half of a block's columns holds its own 64 keys' dS
-        mma_ts<kQB, 64>(tQ, tmem + (j & 1) * 128, umma_desc(smem_u32(sK + j % C::NK * C::TILE), C::CH, 1024), idQ,
-                        kb.width(j), j > 0);
-        umma_commit(j + 1 < kb.n ? &k_empty[j % C::NK] : done);
+        mma_ts<kKB, 64>(tQ, tP, umma_desc(smem_u32(sK + j % NK * C::TILE), C::CH, 1024), idQ, kb.width(j), j > 0);
+        umma_commit(j + 1 < kb.n ? k_empty + j % NK : done);
       }
       __syncwarp();
-      if (j + 2 < kb.n) scores(j + 2);
+      if (j + 1 < kb.n) dprobs(j + 1);
     }
   } else {
-    const int half = (int)(threadIdx.x - 64) >> 7;
+    const int g = (int)(threadIdx.x - 64) >> 7;  // half of the columns
     const int r = (warp & 3) * 32 + lane, i = q0 + r;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const bool live = i < p.S;
     const int64_t t = (int64_t)b * p.S + i;
     const float sl2 = p.scale * kLog2e;
+    const float lse2 = live ? p.lse[t * p.hq + h] * kLog2e : INFINITY;
     // D of the tile's rows, from the forward's unrounded o where it was kept: a warp takes 16 rows, HD / 8
     // lanes a row, every load in flight before the first sum
     {
@@ -555,51 +618,81 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         if (lane % LPR == 0) sD[w8 * 16 + n * RPI + lane / LPR] = sum;
       }
     }
-    const float lse2 = live ? p.lse[t * p.hq + h] * kLog2e : INFINITY;
+    // the first four warps copy Q's rows into TMEM, the others dO's
+    bool ok = warp_wait(q_full, 0);
+    if (ok) {
+      const uint8_t* src = g ? sO : sQ;
+#pragma unroll
+      for (int c = 0; c < HD / 64; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(w + 4 * e) = *reinterpret_cast<const uint4*>(src + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
+        tmem_st32(tA + g * 64 + c * 32 + lanes, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(a_full);
+    }
     asm volatile("bar.sync 1, 256;" ::: "memory");
     const float D = sD[r];
-    if (half == 0) reinterpret_cast<float2*>(p.D)[stat_row(b, h, p.hq, p.S) + i] = make_float2(lse2, D);
-    bool ok = true;
-    // columns [64 half, 64 half + NC) of a block
+    p.D[stat_row(b, h, p.hq, p.S) + g * up(p.S, kQB) + i] = g ? D : lse2;
+    const uint32_t tX = tS + g * 64 + lanes, tY = tP + g * 64 + lanes;
+    // columns [64 g, 64 g + NC) of a block
     const auto block = [&](auto nc, bool masked, int k0, int j) {
       constexpr int NC = decltype(nc)::value;
-      const uint32_t tS = tmem + (j & 1) * 128 + half * 64 + lanes;
       float x[NC], y[NC];
-      tmem_row<NC>(x, tS);
+      tmem_row<NC>(x, tX);
+      tc_fence_before();
+      mbar_arrive(s_free);
 #pragma unroll
       for (int c = 0; c < NC; ++c) x[c] = ex2_approx(fmaf(x[c], sl2, -lse2));
       if (masked) {
-        const int hi = i - k0 - half * 64, lo = hi - p.window, sc = p.sinks - k0 - half * 64;
+        const uint64_t vis = visible_keys(i, k0 + g * 64, p.window, p.sinks);
+        const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-          if (c > hi || (c <= lo && c >= sc)) x[c] = 0.f;
+          if (!(bits[c / 32] >> (c % 32) & 1)) x[c] = 0.f;
       }
       if (!(ok = warp_wait(dp_full, j & 1))) return;
       tc_fence_after();
-      tmem_row<NC>(y, tP + half * 64 + lanes);
+      tmem_row<NC>(y, tY);
       uint32_t w[NC / 2];
 #pragma unroll
       for (int c = 0; c < NC / 2; ++c) w[c] = pack2(x[2 * c] * (y[2 * c] - D), x[2 * c + 1] * (y[2 * c + 1] - D));
 #pragma unroll
-      for (int c = 0; c < NC / 2; c += 16) tmem_st16(tS + c, w + c);
+      for (int c = 0; c < NC / 2; c += 16) tmem_st16(tY + c, w + c);
       tmem_st_wait();
     };
     for (int j = 0; j < kb.n && ok; ++j) {
-      if (!(ok = warp_wait(&s_full[j & 1], (j >> 1) & 1))) break;
+      if (!(ok = warp_wait(s_full, j & 1))) break;
       tc_fence_after();
-      const int k0 = kb.k0(j), w = kb.width(j);
-      if (w > 32) block(std::integral_constant<int, 64>{}, !all_visible(q0, kQB, k0, kQB, p.window, p.sinks), k0, j);
-      else if (half == 0) block(std::integral_constant<int, 32>{}, true, k0, j);
-      else ok = warp_wait(dp_full, j & 1);
+      const int k0 = kb.k0(j);
+      if (kb.width(j) > 32) {
+        block(std::integral_constant<int, 64>{}, !all_visible(q0, kQB, k0, kKB, p.window, p.sinks), k0, j);
+      } else if (g == 0) {
+        block(std::integral_constant<int, 32>{}, true, k0, j);
+      } else {
+        mbar_arrive(s_free);
+        ok = warp_wait(dp_full, j & 1);
+      }
       tc_fence_before();
       mbar_arrive(ds_full);
     }
-    if (ok && warp_wait(done, 0)) {
+    ok = ok && warp_wait(done, 0);
+    if (ok) {  // Q's shared memory takes the tile of dQ
       tc_fence_after();
       float lo[HD / 4], hi[HD / 4];
-      tmem_row<HD / 4>(lo, tQ + half * (HD / 4) + lanes);
-      tmem_row<HD / 4>(hi, tQ + half * (HD / 4) + HD / 2 + lanes);
-      if (live) store_grad<HD>(p.dq + t * p.lddq + (int64_t)h * HD, lo, hi, p, i, half);
+      tmem_row<HD / 4>(lo, tQ + g * (HD / 4) + lanes);
+      tmem_row<HD / 4>(hi, tQ + g * (HD / 4) + HD / 2 + lanes);
+      stage_grad<HD>(sQ, C::CH, r, lo, hi, p, i, g);
+      fence_proxy_async();
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (warp == 2 && ok && elect_one()) {
+#pragma unroll
+      for (int c = 0; c < HD / 64; ++c) tma_store_3d(&tmDq, sQ + c * C::CH, h * HD + c * 64, q0, b);
+      tma_store_wait();
     }
   }
   __syncwarp();
@@ -612,7 +705,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
 }
 
 // ---------------------------------------------------------------------------------- dK, dV
-// The work of one key tile of a kv head: its group's heads times the 64-row query blocks that see any
+// The work of one key tile of a kv head: its group's heads times the 128-row query blocks that see any
 // of its keys. It is cut into parts of equal length (n for the tiles that hold sinks, whose queries
 // reach to the end of the sequence, n for the others); with one part a CTA stores dK and dV itself,
 // else its fp32 sums go to the scratch and k_window_join adds them in order.
@@ -623,7 +716,7 @@ struct Split {
   int ps, pw;      // parts of a tile with sinks, of another
   __host__ __device__ int ctas() const { return nsb * ps + (nkb - nsb) * pw; }  // a sequence and kv head
   __host__ __device__ int blocks(int kb) const {
-    const int n = nq - 2 * kb;
+    const int n = nq - kb;
     return kb < nsb || n < near ? n : near;
   }
 };
@@ -634,31 +727,34 @@ __host__ __device__ __forceinline__ int64_t joined_parts(const Split& s) {
 
 template <int HD>
 struct DkvCfg {
-  static constexpr int QB = 64, NS = 3;                       // rows of a query block, blocks in flight
-  static constexpr uint32_t CH = kQB * 128, QCH = QB * 128;  // [128 x 64], [64 x 64] bf16
-  static constexpr uint32_t KT = (HD / 64) * CH, QT = (HD / 64) * QCH;
-  static constexpr uint32_t STAGE = 2 * QT + QB * 8;  // Q, dO, (lse, D)
-  static constexpr uint32_t STEP = (STAGE + 1023) / 1024 * 1024;
-  static constexpr uint32_t SMEM = 2 * KT + NS * STEP + 1024 + 256;
-  static constexpr uint32_t COLS = 2 * 128 + 2 * HD <= 256 ? 256 : 512;
+  static constexpr int QB = 128, NS = 2;                    // rows of a query block, blocks in flight
+  static constexpr uint32_t CH = kQB * 128;                // [128 x 64] bf16
+  static constexpr uint32_t TILE = (HD / 64) * CH;
+  static constexpr uint32_t STAGE = 2 * TILE + 2 * QB * 4;  // Q, dO, lse, D
+  static constexpr uint32_t SMEM = 2 * TILE + NS * STAGE + 1024 + 256;
 };
 
 // 320 threads: warp 0 TMA, warp 1 the MMAs, warps 2-9 two threads a key row (half a block's queries each).
-//   S^T = K Q^T and dP^T = V dO^T into one of two TMEM buffer pairs; P^T and dS^T as bf16 over the
-//   threads' own columns of them, the A operands of dV += P^T dO and dK += dS^T Q (Q and dO read
-//   MN-major from the tiles used K-major above). While the threads work on block j, the tensor cores
-//   form the sums of j - 1 and the scores of j + 1.
+//   S^T = K Q^T, P^T = 2^(S' - lse') as bf16 over it, the A operand of dV += P^T dO;
+//   dP^T = V dO^T, dS^T = P^T (dP^T - D) as bf16 over it, the A operand of dK += dS^T Q
+// (Q and dO read MN-major from the tiles used K-major for the scores). With dV, dK and both scores TMEM
+// is full. The threads turn S and dP in two steps, so that the tensor cores form dV of j and S of j + 1
+// under the second, dK of j and dP of j + 1 under the first step of j + 1. (Blocks of 64 queries with two
+// buffers of each took 2000 clocks a block and thus 4000 for these 128 queries: at N = 64 an MMA
+// is bound by shared memory, 48 clocks for 32, and by its issue.)
 template <int HD>
 __global__ void __launch_bounds__(320, 1)
 k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
-              const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const WinBwdArgs p,
+              const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+              const __grid_constant__ CUtensorMap tmDk, const __grid_constant__ CUtensorMap tmDv, const WinBwdArgs p,
               const Split sp, float* __restrict__ parts) {
   using C = DkvCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sK = smem, *sV = smem + C::KT, *sQ = smem + 2 * C::KT;  // [NS] stages
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sQ + C::NS * C::STEP);
-  uint64_t *kv_full = bars, *done = bars + 1, *s_full = bars + 2, *t_full = bars + 4, *q_full = bars + 6,
+  uint8_t *sK = smem, *sV = smem + C::TILE, *sQ = smem + 2 * C::TILE;  // [NS] stages
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sQ + C::NS * C::STAGE);
+  uint64_t *p_full = bars, *ds_full = bars + 1;  // of all 256 row threads
+  uint64_t *kv_full = bars + 2, *done = bars + 3, *s_full = bars + 4, *dp_full = bars + 5, *q_full = bars + 6,
            *q_empty = bars + 6 + C::NS;
   constexpr int kBars = 6 + 2 * C::NS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
@@ -678,7 +774,7 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   const auto query = [&](int j) { return k0 + (it0 + j) % nqb * C::QB; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kBars; ++i) mbar_init(bars + i, bars + i == t_full || bars + i == t_full + 1 ? 256 : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(bars + i, i < 2 ? 256 : 1);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -686,15 +782,17 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     tma_prefetch_desc(&tmO);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmDk);
+    tma_prefetch_desc(&tmDv);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::COLS);
+    tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot, tV = tmem + 256, tK = tmem + 256 + HD;  // S^T at 0, 64; dP^T at 128, 192
+  const uint32_t tmem = *tmem_slot, tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
   pdl_wait();
   pdl_trigger();
 
@@ -702,7 +800,7 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     // nothing of the work fell to this part
   } else if (warp == 0) {
     if (elect_one()) {
-      mbar_arrive_expect_tx(kv_full, 2 * C::KT);
+      mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
       load_tile<HD>(sK, C::CH, &tmK, kv_full, kvh * HD, k0, b);
       load_tile<HD>(sV, C::CH, &tmV, kv_full, kvh * HD, k0, b);
     }
@@ -711,102 +809,124 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       const int s = j % C::NS, h = head(j), q = query(j);
       if (j >= C::NS && !warp_wait(&q_empty[s], (j / C::NS - 1) & 1)) break;
       if (elect_one()) {
-        uint8_t* st = sQ + s * C::STEP;
+        uint8_t* st = sQ + s * C::STAGE;
+        const float* stat = p.D + stat_row(b, h, p.hq, p.S) + q;
         mbar_arrive_expect_tx(&q_full[s], C::STAGE);
-        load_tile<HD>(st, C::QCH, &tmQ, &q_full[s], h * HD, q, b);
-        load_tile<HD>(st + C::QT, C::QCH, &tmO, &q_full[s], h * HD, q, b);
-        bulk_load(st + 2 * C::QT, reinterpret_cast<const float2*>(p.D) + stat_row(b, h, p.hq, p.S) + q, C::QB * 8,
-                  &q_full[s]);
+        load_tile<HD>(st, C::CH, &tmQ, &q_full[s], h * HD, q, b);
+        bulk_load(st + 2 * C::TILE, stat, C::QB * 4, &q_full[s]);
+        bulk_load(st + 2 * C::TILE + C::QB * 4, stat + up(p.S, kQB), C::QB * 4, &q_full[s]);
+        load_tile<HD>(st + C::TILE, C::CH, &tmO, &q_full[s], h * HD, q, b);
       }
       __syncwarp();
     }
   } else if (warp == 1) {
     constexpr uint32_t idS = umma_idesc_bf16(128, C::QB, 0, 0), idG = umma_idesc_bf16(128, HD, 0, 1);
     bool ok = warp_wait(kv_full, 0);
-    for (int j = 0; j < n + 2 && ok; ++j) {
-      if (j >= 2) {  // dV += P^T dO, dK += dS^T Q of block j - 2
-        const int i = j - 2, st = i & 1;
-        if (!(ok = warp_wait(&t_full[st], (i >> 1) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {  // the second half of the queries lies 32 columns further
-          const uint64_t q = umma_desc(smem_u32(sQ + i % C::NS * C::STEP), C::QCH, 1024);
-          mma_ts<C::QB, 32>(tV, tmem + st * 64, at(q, C::QT), idG, C::QB, i > 0);
-          mma_ts<C::QB, 32>(tK, tmem + 128 + st * 64, q, idG, C::QB, i > 0);
-          umma_commit(i + 1 < n ? &q_empty[i % C::NS] : done);
-        }
-        __syncwarp();
+    const auto stage = [&](int j) { return smem_u32(sQ + j % C::NS * C::STAGE); };
+    const auto scores = [&](int j) {  // S^T_j = K Q_j^T
+      if (!(ok = ok && warp_wait(&q_full[j % C::NS], (j / C::NS) & 1))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_ss<HD>(tS, umma_desc(smem_u32(sK), 16, 1024), C::CH, umma_desc(stage(j), 16, 1024), C::CH, idS);
+        umma_commit(s_full);
       }
-      if (j < n) {  // S^T_j = K Q_j^T, dP^T_j = V dO_j^T
-        const int st = j & 1;
-        if (!(ok = warp_wait(&q_full[j % C::NS], (j / C::NS) & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t q = umma_desc(smem_u32(sQ + j % C::NS * C::STEP), 16, 1024);
-          mma_ss<HD>(tmem + st * 64, umma_desc(smem_u32(sK), 16, 1024), C::CH, q, C::QCH, idS);
-          mma_ss<HD>(tmem + 128 + st * 64, umma_desc(smem_u32(sV), 16, 1024), C::CH, at(q, C::QT), C::QCH, idS);
-          umma_commit(&s_full[st]);
-        }
-        __syncwarp();
+      __syncwarp();
+    };
+    const auto dprobs = [&](int j) {  // dP^T_j = V dO_j^T
+      if (elect_one()) {
+        mma_ss<HD>(tP, umma_desc(smem_u32(sV), 16, 1024), C::CH, umma_desc(stage(j) + C::TILE, 16, 1024), C::CH, idS);
+        umma_commit(dp_full);
       }
+      __syncwarp();
+    };
+    scores(0);
+    if (ok) dprobs(0);
+    for (int j = 0; j < n && ok; ++j) {  // each half of a block's columns holds its own 64 queries' P and dS
+      if (!(ok = warp_wait(p_full, j & 1))) break;
+      tc_fence_after();
+      if (elect_one()) mma_ts<C::QB, 64>(tV, tS, umma_desc(stage(j) + C::TILE, C::CH, 1024), idG, C::QB, j > 0);
+      __syncwarp();
+      if (j + 1 < n) scores(j + 1);
+      if (!(ok = ok && warp_wait(ds_full, j & 1))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_ts<C::QB, 64>(tK, tP, umma_desc(stage(j), C::CH, 1024), idG, C::QB, j > 0);
+        umma_commit(j + 1 < n ? &q_empty[j % C::NS] : done);
+      }
+      __syncwarp();
+      if (j + 1 < n) dprobs(j + 1);
     }
   } else {
     const int half = (int)(threadIdx.x - 64) >> 7;
     const int r = (warp & 3) * 32 + lane, key = k0 + r;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tX = tS + half * 64 + lanes, tY = tP + half * 64 + lanes;
     const float sl2 = p.scale * kLog2e;
     bool ok = true;
     for (int j = 0; j < n && ok; ++j) {
-      const int st = j & 1, q = query(j) + half * 32;  // this thread's first query
-      if (!(ok = warp_wait(&q_full[j % C::NS], (j / C::NS) & 1) && warp_wait(&s_full[st], (j >> 1) & 1))) break;
+      const int q = query(j);
+      if (!(ok = warp_wait(&q_full[j % C::NS], (j / C::NS) & 1) && warp_wait(s_full, j & 1))) break;
       tc_fence_after();
-      const float4* stat = reinterpret_cast<const float4*>(sQ + (j % C::NS) * C::STEP + 2 * C::QT) + half * 16;
-      const uint32_t tS = tmem + st * 64 + half * 32 + lanes, tP = tS + 128;
-      float a[32], d[32];
-      tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(a));
-      tmem_ld32(tP, *reinterpret_cast<uint32_t(*)[32]>(d));
-      tmem_ld_wait();
-      const bool masked = !all_visible(query(j), C::QB, k0, kQB, p.window, p.sinks);
-      // visible queries of this key: [key, key + window), from key on where it is a sink
-      const int lo = key - q, hi = key < p.sinks ? C::QB : lo + p.window;
-      uint32_t w[16], u[16];
+      // lse and D of this thread's 64 queries
+      const float4* lse = reinterpret_cast<const float4*>(sQ + j % C::NS * C::STAGE + 2 * C::TILE) + half * 16;
+      const float4* del = lse + C::QB / 4;
+      float x[64], y[64];
+      uint32_t w[32];
+      tmem_row<64>(x, tX);
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        const float4 s2 = stat[c / 2];  // (lse, D) of two queries
-        float p0 = ex2_approx(fmaf(a[c], sl2, -s2.x)), p1 = ex2_approx(fmaf(a[c + 1], sl2, -s2.z));
-        if (masked) {
-          if (c < lo || c >= hi) p0 = 0.f;
-          if (c + 1 < lo || c + 1 >= hi) p1 = 0.f;
-        }
-        w[c / 2] = pack2(p0, p1);
-        u[c / 2] = pack2(p0 * (d[c] - s2.y), p1 * (d[c + 1] - s2.w));
+      for (int c = 0; c < 64; c += 4) {
+        const float4 l4 = lse[c / 4];
+        x[c] = ex2_approx(fmaf(x[c], sl2, -l4.x));
+        x[c + 1] = ex2_approx(fmaf(x[c + 1], sl2, -l4.y));
+        x[c + 2] = ex2_approx(fmaf(x[c + 2], sl2, -l4.z));
+        x[c + 3] = ex2_approx(fmaf(x[c + 3], sl2, -l4.w));
       }
-      tmem_st16(tS, w);
-      tmem_st16(tP, u);
+      if (!all_visible(q, C::QB, k0, kQB, p.window, p.sinks)) {
+        const uint64_t vis = visible_queries(key, q + half * 64, p.window, p.sinks);
+        const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (!(bits[c / 32] >> (c % 32) & 1)) x[c] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 32; ++c) w[c] = pack2(x[2 * c], x[2 * c + 1]);
+      tmem_st16(tX, w);
+      tmem_st16(tX + 16, w + 16);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&t_full[st]);
-    }
-    if (ok && warp_wait(done, 0)) {
+      mbar_arrive(p_full);
+      if (!(ok = warp_wait(dp_full, j & 1))) break;
       tc_fence_after();
-      if (np == 1) {
-        const bool live = key < p.S;
-        const int64_t t = (int64_t)b * p.S + key;
+      tmem_row<64>(y, tY);
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 d4 = del[c / 4];
+        w[c / 2] = pack2(x[c] * (y[c] - d4.x), x[c + 1] * (y[c + 1] - d4.y));
+        w[c / 2 + 1] = pack2(x[c + 2] * (y[c + 2] - d4.z), x[c + 3] * (y[c + 3] - d4.w));
+      }
+      tmem_st16(tY, w);
+      tmem_st16(tY + 16, w + 16);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(ds_full);
+    }
+    ok = ok && warp_wait(done, 0);
+    if (ok) {
+      tc_fence_after();
+      if (np == 1) {  // K's and V's shared memory takes the tiles of dK and dV
         float x0[HD / 4], x1[HD / 4];
         tmem_row<HD / 4>(x0, tK + half * (HD / 4) + lanes);
         tmem_row<HD / 4>(x1, tK + half * (HD / 4) + HD / 2 + lanes);
-        if (live) store_grad<HD>(p.dk + t * p.lddk + (int64_t)kvh * HD, x0, x1, p, key, half);
-        __nv_bfloat16* dst = p.dv + t * p.lddv + (int64_t)kvh * HD + half * (HD / 2);
+        stage_grad<HD>(sK, C::CH, r, x0, x1, p, key, half);
+        if (HD == 128 || half == 0) {
+          float v[64];
+          uint32_t w[32];
+          tmem_row<64>(v, tV + half * 64 + lanes);
 #pragma unroll
-        for (int c = 0; c < HD / 2; c += 32) {
-          float v[32];
-          tmem_row<32>(v, tV + half * (HD / 2) + c + lanes);
-          if (live) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(pack2(v[e], v[e + 1]), pack2(v[e + 2], v[e + 3]),
-                                                                  pack2(v[e + 4], v[e + 5]), pack2(v[e + 6], v[e + 7]));
-          }
+          for (int e = 0; e < 32; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1]);
+          stage_row(sV + half * C::CH, r, w);
         }
+        fence_proxy_async();
       } else {  // [key row][dK, dV]
         const int64_t at = (int64_t)bk * joined_parts(sp) + (sink || sp.ps == 1 ? y : (int64_t)sp.nsb * sp.ps + y);
         float* dst = parts + (at * kQB + r) * (2 * HD) + half * HD;
@@ -819,13 +939,22 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         }
       }
     }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (warp == 2 && ok && np == 1 && elect_one()) {
+#pragma unroll
+      for (int c = 0; c < HD / 64; ++c) {
+        tma_store_3d(&tmDk, sK + c * C::CH, kvh * HD + c * 64, k0, b);
+        tma_store_3d(&tmDv, sV + c * C::CH, kvh * HD + c * 64, k0, b);
+      }
+      tma_store_wait();
+    }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::COLS);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -878,7 +1007,7 @@ __global__ void __launch_bounds__(256) k_window_join(const WinBwdArgs p, const S
 }
 
 // How the dK / dV work is cut: the parts of a tile are chosen for the fewest rounds of a B200's SMs times
-// what a round takes, a CTA costing about 6 blocks besides its own (start, tiles of K and V, stores).
+// what a round takes, a CTA costing about 3 blocks besides its own (start, tiles of K and V, stores).
 Split plan_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
   constexpr int sms = 148;
   const int64_t B = T / S;
@@ -886,16 +1015,16 @@ Split plan_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
   Split s;
   s.nkb = (S + kQB - 1) / kQB;
   s.nsb = (int)(((int64_t)std::min(sinks, S) + kQB - 1) / kQB);
-  s.nq = (S + 63) / 64;
-  s.near = (int)std::min<int64_t>(s.nq, ((int64_t)kQB - 2 + std::min(window, S)) / 64 + 1);
+  s.nq = s.nkb;
+  s.near = (int)std::min<int64_t>(s.nq, ((int64_t)kQB - 2 + std::min(window, S)) / kQB + 1);
   const int64_t tw = (int64_t)grp * s.near, ts = (int64_t)grp * s.nq;
   int64_t best = INT64_MAX;
   s.ps = s.pw = 1;
-  for (int n = 1; n <= 16 && (n == 1 || tw / n >= 4); ++n) {
+  for (int n = 1; n <= 16 && (n == 1 || tw / n >= 2); ++n) {
     const int64_t len = (tw + n - 1) / n;
     const int64_t ps = std::min<int64_t>((ts + len - 1) / len, 4096);
     const int64_t ctas = B * hkv * (s.nsb * ps + (int64_t)(s.nkb - s.nsb) * n);
-    const int64_t cost = ((ctas + sms - 1) / sms) * (len + 6);
+    const int64_t cost = ((ctas + sms - 1) / sms) * (len + 3);
     if (cost < best) {
       best = cost;
       s.ps = (int)ps;
@@ -930,16 +1059,16 @@ template <int HD>
 cudaError_t launch_fwd(const WinArgs& a, cudaStream_t s) {
   using C = FwdCfg<HD>;
   const int64_t B = a.T / a.S, cq = (int64_t)a.hq * HD, ck = (int64_t)a.hkv * HD;
-  CUtensorMap q, k, v, k16, v16;
-  if (!make_map3(&q, a.q, B, a.S, cq, a.ldq, kQB) || !make_map3(&k, a.k, B, a.S, ck, a.ldk, kQB) ||
-      !make_map3(&v, a.v, B, a.S, ck, a.ldv, kQB) || !make_map3(&k16, a.k, B, a.S, ck, a.ldk, 16) ||
-      !make_map3(&v16, a.v, B, a.S, ck, a.ldv, 16))
+  CUtensorMap q, k, v, k16, v16, o;
+  if (!make_map3(&q, a.q, B, a.S, cq, a.ldq, kQB) || !make_map3(&k, a.k, B, a.S, ck, a.ldk, C::KB) ||
+      !make_map3(&v, a.v, B, a.S, ck, a.ldv, C::KB) || !make_map3(&k16, a.k, B, a.S, ck, a.ldk, 16) ||
+      !make_map3(&v16, a.v, B, a.S, ck, a.ldv, 16) || !make_map3(&o, a.o, B, a.S, cq, a.ldo, kQB))
     return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(k_window_fwd<HD>, C::SMEM, done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = B * a.hq * ((a.S + kQB - 1) / kQB);
-  return launch_k(k_window_fwd<HD>, dim3((unsigned)tiles), dim3(192), C::SMEM, s, 0, q, k, v, k16, v16, a);
+  return launch_k(k_window_fwd<HD>, dim3((unsigned)tiles), dim3(192), C::SMEM, s, 0, q, k, v, k16, v16, o, a);
 }
 
 template <int HD>
@@ -947,23 +1076,24 @@ cudaError_t launch_bwd(const WinBwdArgs& a, cudaStream_t s) {
   using Q = DqCfg<HD>;
   using K = DkvCfg<HD>;
   const int64_t B = a.T / a.S, cq = (int64_t)a.hq * HD, ck = (int64_t)a.hkv * HD;
-  CUtensorMap q, o, k, v, k16, v16, q64, o64;
+  CUtensorMap q, o, k, v, k16, v16, dq, dk, dv;
   if (!make_map3(&q, a.q, B, a.S, cq, a.ldq, kQB) || !make_map3(&o, a.dout, B, a.S, cq, a.lddo, kQB) ||
-      !make_map3(&k, a.k, B, a.S, ck, a.ldk, kQB) || !make_map3(&v, a.v, B, a.S, ck, a.ldv, kQB) ||
+      !make_map3(&k, a.k, B, a.S, ck, a.ldk, Q::KB) || !make_map3(&v, a.v, B, a.S, ck, a.ldv, Q::KB) ||
       !make_map3(&k16, a.k, B, a.S, ck, a.ldk, 16) || !make_map3(&v16, a.v, B, a.S, ck, a.ldv, 16) ||
-      !make_map3(&q64, a.q, B, a.S, cq, a.ldq, K::QB) || !make_map3(&o64, a.dout, B, a.S, cq, a.lddo, K::QB))
+      !make_map3(&dq, a.dq, B, a.S, cq, a.lddq, kQB) || !make_map3(&dk, a.dk, B, a.S, ck, a.lddk, kQB) ||
+      !make_map3(&dv, a.dv, B, a.S, ck, a.lddv, kQB))
     return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> done_q{0}, done_k{0};
   cudaError_t e = allow_smem(k_window_dq<HD>, Q::SMEM, done_q);
   if (e == cudaSuccess) e = allow_smem(k_window_dkdv<HD>, K::SMEM, done_k);
   if (e != cudaSuccess) return e;
   const int64_t tiles = B * a.hq * ((a.S + kQB - 1) / kQB);
-  e = launch_k(k_window_dq<HD>, dim3((unsigned)tiles), dim3(320), Q::SMEM, s, 0, q, o, k, v, k16, v16, a);
+  e = launch_k(k_window_dq<HD>, dim3((unsigned)tiles), dim3(320), Q::SMEM, s, 0, q, o, k, v, k16, v16, dq, a);
   note_launch(1);
   if (e != cudaSuccess) return e;
   const Split sp = plan_split(a.T, a.S, a.hq, a.hkv, a.window, a.sinks);
   float* parts = a.D + 2 * B * a.hq * up(a.S, kQB);
-  e = launch_k(k_window_dkdv<HD>, dim3((unsigned)(B * a.hkv * sp.ctas())), dim3(320), K::SMEM, s, 0, q64, o64, k, v, a, sp,
+  e = launch_k(k_window_dkdv<HD>, dim3((unsigned)(B * a.hkv * sp.ctas())), dim3(320), K::SMEM, s, 0, q, o, k, v, dk, dv, a, sp,
                parts);
   note_launch(1);
   if (e != cudaSuccess || joined_parts(sp) == 0) return e;
