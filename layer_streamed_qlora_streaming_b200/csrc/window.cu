@@ -35,18 +35,39 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// D += A B with A [128, 16] bf16 in TMEM (two values a column, row = lane) and B by descriptor
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+// A shared-memory matrix descriptor with its 32-bit halves apart: only the low one, which holds the
+// address, differs between the tiles and steps of a product.
+struct Desc {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc make_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  const uint64_t d = umma_desc(saddr, lbo_bytes, sbo_bytes);
+  return {(uint32_t)d, (uint32_t)(d >> 32)};
+}
+__device__ __forceinline__ Desc at(Desc d, uint32_t bytes) { return {d.lo + (bytes >> 4), d.hi}; }
+// D (+)= A B with A [128, 16] bf16 in TMEM (two values a column, row = lane) and B by descriptor
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, Desc b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(db), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], x, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// The descriptor of a tile `bytes` further. Descriptors are made once a block: building two for every MMA
-// cost the issuing thread about 110 cycles each, of the 64 that an MMA of 128 x 128 x 16 takes.
-__device__ __forceinline__ uint64_t at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+// the same with A by descriptor
+__device__ __forceinline__ void umma_ss(uint32_t d, Desc a, Desc b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 x, {%1, %2};\n\t"
+      "mov.b64 y, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+      "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// x, the same in every lane, as a value that the compiler too knows to be the same
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 // True for one lane of a converged warp, always the same one. The TMA and MMA warps run their loops with all
 // lanes and issue under this, so that no lane runs ahead while the instructions' uniform operands live.
 __device__ __forceinline__ bool elect_one() {
@@ -150,21 +171,21 @@ __device__ __forceinline__ void tma_store_wait() {
 }
 // D = A B^T over HD columns, A in TMEM (HD / 2 columns), B K-major in chunks of 64 columns
 template <int HD>
-__device__ __forceinline__ void mma_tt(uint32_t d, uint32_t a, uint64_t bb, uint32_t bchunk, uint32_t id) {
+__device__ __forceinline__ void mma_tt(uint32_t d, uint32_t a, Desc bb, uint32_t bchunk, uint32_t id) {
 #pragma unroll
   for (int kk = 0; kk < HD / 16; ++kk) umma_ts(d, a + kk * 8, at(bb, (kk >> 2) * bchunk + (kk & 3) * 32), id, kk != 0);
 }
 // D = A B^T over HD columns, both K-major in chunks of 64 columns
 template <int HD>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint32_t achunk, uint64_t bb, uint32_t bchunk, uint32_t id) {
+__device__ __forceinline__ void mma_ss(uint32_t d, Desc a, uint32_t achunk, Desc bb, uint32_t bchunk, uint32_t id) {
 #pragma unroll
   for (int kk = 0; kk < HD / 16; ++kk)
-    umma_bf16(d, at(a, (kk >> 2) * achunk + (kk & 3) * 32), at(bb, (kk >> 2) * bchunk + (kk & 3) * 32), id, kk != 0);
+    umma_ss(d, at(a, (kk >> 2) * achunk + (kk & 3) * 32), at(bb, (kk >> 2) * bchunk + (kk & 3) * 32), id, kk != 0);
 }
 // D (+)= A B over w <= N rows of B (MN-major, 128-byte rows): A bf16 in TMEM, 16 rows of B every 8 columns; with HALF,
 // rows [HALF, ...) of it HALF columns behind the first
 template <int N, int HALF>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bb, uint32_t id, int w, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc bb, uint32_t id, int w, bool add) {
   const auto step = [&](int kk, uint32_t acc) {
     umma_ts(d, a + (HALF ? kk * 16 / HALF * HALF + kk * 16 % HALF / 2 : kk * 8), at(bb, kk * 16 * 128), id, acc);
   };
@@ -213,7 +234,7 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
   const int b = u / nq, q0 = (nq - 1 - u % nq) * kQB;
   const int kvh = h / (p.hq / p.hkv);
   const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 14; ++i) mbar_init(bars + i, i >= 12 ? 128 : 1);
@@ -232,7 +253,7 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tS = *tmem_slot, tO = tS + 128;
+  const uint32_t tS = uniform(*tmem_slot), tO = tS + 128;
   pdl_wait();
   pdl_trigger();
 
@@ -261,7 +282,7 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       if (!(ok = ok && warp_wait(k_full + s, (j >> 1) & 1))) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_ss<HD>(tS + s * kKB, umma_desc(smem_u32(sQ), 16, 1024), C::CH, umma_desc(smem_u32(sK + s * C::KT), 16, 1024),
+        mma_ss<HD>(tS + s * kKB, make_desc(smem_u32(sQ), 16, 1024), C::CH, make_desc(smem_u32(sK + s * C::KT), 16, 1024),
                    C::KCH, umma_idesc_bf16(128, kb.width(j), 0, 0));
         umma_commit(s_full + s);
         umma_commit(k_empty + s);
@@ -275,7 +296,7 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       if (!(ok = warp_wait(v_full + s, (j >> 1) & 1) && warp_wait(p_full + s, (j >> 1) & 1))) break;
       tc_fence_after();
       if (elect_one()) {  // O += P_j V_j
-        mma_ts<kKB, 0>(tO, tS + s * kKB, umma_desc(smem_u32(sV + s * C::KT), C::KCH, 1024), idO, kb.width(j), j > 0);
+        mma_ts<kKB, 0>(tO, tS + s * kKB, make_desc(smem_u32(sV + s * C::KT), C::KCH, 1024), idO, kb.width(j), j > 0);
         umma_commit(j + 1 < kb.n ? v_empty + s : o_full);
       }
       __syncwarp();
@@ -488,7 +509,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   const int b = u / nq, q0 = (nq - 1 - u % nq) * kQB;
   const int kvh = h / (p.hq / p.hkv);
   const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) mbar_init(bars + i, i < 3 ? 256 : 1);
@@ -509,7 +530,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   __syncthreads();
   tc_fence_after();
   // Q and dO (64 columns each), S, dP, dQ
-  const uint32_t tmem = *tmem_slot, tA = tmem, tS = tmem + 128, tP = tmem + 256, tQ = tmem + 384;
+  const uint32_t tmem = uniform(*tmem_slot), tA = tmem, tS = tmem + 128, tP = tmem + 256, tQ = tmem + 384;
   pdl_wait();
   pdl_trigger();
 
@@ -540,7 +561,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       if (!(ok = ok && warp_wait(k_full + s, (j / NK) & 1))) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_tt<HD>(tS, tA, umma_desc(smem_u32(sK + s * C::TILE), 16, 1024), C::CH, umma_idesc_bf16(128, kb.width(j), 0, 0));
+        mma_tt<HD>(tS, tA, make_desc(smem_u32(sK + s * C::TILE), 16, 1024), C::CH, umma_idesc_bf16(128, kb.width(j), 0, 0));
         umma_commit(s_full);
       }
       __syncwarp();
@@ -550,7 +571,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       if (!(ok = ok && warp_wait(v_full + s, (j / NV) & 1))) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_tt<HD>(tP, tA + 64, umma_desc(smem_u32(sV + s * C::TILE), 16, 1024), C::CH,
+        mma_tt<HD>(tP, tA + 64, make_desc(smem_u32(sV + s * C::TILE), 16, 1024), C::CH,
                    umma_idesc_bf16(128, kb.width(j), 0, 0));
         umma_commit(dp_full);
         umma_commit(v_empty + s);
@@ -567,7 +588,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       if (!(ok = ok && warp_wait(ds_full, j & 1))) break;
       tc_fence_after();
       if (elect_one()) {  // each half of a block's columns holds its own 64 keys' dS
-        mma_ts<kKB, 64>(tQ, tP, umma_desc(smem_u32(sK + j % NK * C::TILE), C::CH, 1024), idQ, kb.width(j), j > 0);
+        mma_ts<kKB, 64>(tQ, tP, make_desc(smem_u32(sK + j % NK * C::TILE), C::CH, 1024), idQ, kb.width(j), j > 0);
         umma_commit(j + 1 < kb.n ? k_empty + j % NK : done);
       }
       __syncwarp();
@@ -768,7 +789,7 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   const int k0 = kb * kQB, nqb = sp.blocks(kb);
   const int64_t total = (int64_t)grp * nqb;
   const int it0 = (int)(total * part / np), n = (int)(total * (part + 1) / np) - it0;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   // item j of this CTA: its head and first query
   const auto head = [&](int j) { return kvh * grp + (it0 + j) / nqb; };
   const auto query = [&](int j) { return k0 + (it0 + j) % nqb * C::QB; };
@@ -792,7 +813,7 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot, tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
+  const uint32_t tmem = uniform(*tmem_slot), tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
   pdl_wait();
   pdl_trigger();
 
@@ -827,14 +848,14 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       if (!(ok = ok && warp_wait(&q_full[j % C::NS], (j / C::NS) & 1))) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_ss<HD>(tS, umma_desc(smem_u32(sK), 16, 1024), C::CH, umma_desc(stage(j), 16, 1024), C::CH, idS);
+        mma_ss<HD>(tS, make_desc(smem_u32(sK), 16, 1024), C::CH, make_desc(stage(j), 16, 1024), C::CH, idS);
         umma_commit(s_full);
       }
       __syncwarp();
     };
     const auto dprobs = [&](int j) {  // dP^T_j = V dO_j^T
       if (elect_one()) {
-        mma_ss<HD>(tP, umma_desc(smem_u32(sV), 16, 1024), C::CH, umma_desc(stage(j) + C::TILE, 16, 1024), C::CH, idS);
+        mma_ss<HD>(tP, make_desc(smem_u32(sV), 16, 1024), C::CH, make_desc(stage(j) + C::TILE, 16, 1024), C::CH, idS);
         umma_commit(dp_full);
       }
       __syncwarp();
@@ -844,13 +865,13 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     for (int j = 0; j < n && ok; ++j) {  // each half of a block's columns holds its own 64 queries' P and dS
       if (!(ok = warp_wait(p_full, j & 1))) break;
       tc_fence_after();
-      if (elect_one()) mma_ts<C::QB, 64>(tV, tS, umma_desc(stage(j) + C::TILE, C::CH, 1024), idG, C::QB, j > 0);
+      if (elect_one()) mma_ts<C::QB, 64>(tV, tS, make_desc(stage(j) + C::TILE, C::CH, 1024), idG, C::QB, j > 0);
       __syncwarp();
       if (j + 1 < n) scores(j + 1);
       if (!(ok = ok && warp_wait(ds_full, j & 1))) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_ts<C::QB, 64>(tK, tP, umma_desc(stage(j), C::CH, 1024), idG, C::QB, j > 0);
+        mma_ts<C::QB, 64>(tK, tP, make_desc(stage(j), C::CH, 1024), idG, C::QB, j > 0);
         umma_commit(j + 1 < n ? &q_empty[j % C::NS] : done);
       }
       __syncwarp();
