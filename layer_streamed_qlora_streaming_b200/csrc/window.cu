@@ -31,6 +31,65 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kQB = 128;  // rows of a tile in TMEM: queries (forward, dQ) or keys (dK, dV)
 
+// Two fp32 values as one operand of the packed instructions.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 2^x of a pair on the FMA pipe: x = n + f with n the nearest whole number (by adding 1.5 * 2^23, whose low
+// bits then hold n), 2^f on [-1/2, 1/2] by the polynomial of degree 4 of least relative error (2.7e-6, by
+// Remez' exchange), n added to its exponent. x up to 120; what lies below -125 counts as -125. The
+// exponential unit gives 16 values a clock and SM, so a tile of 128 x 128 takes it 1024 clocks, as long as
+// two of its matrix products: a share of the pairs goes this way.
+__device__ __forceinline__ void ex2_pair(uint64_t x, float& r0, float& r1) {
+  constexpr float kMagic = 12582912.f;
+  float x0, x1;
+  unpack(x, x0, x1);
+  x = f2(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
+  const uint64_t t = add2(x, f2(kMagic, kMagic)), f = add2(x, mul2(add2(t, f2(-kMagic, -kMagic)), f2(-1.f, -1.f)));
+  uint64_t q = fma2(f, f2(0.009570102f, 0.009570102f), f2(0.05591786f, 0.05591786f));
+  q = fma2(q, f, f2(0.24024744f, 0.24024744f));
+  q = fma2(q, f, f2(0.6931218f, 0.6931218f));
+  q = fma2(q, f, f2(0.9999993f, 0.9999993f));
+  float t0, t1, q0, q1;
+  unpack(t, t0, t1);
+  unpack(q, q0, q1);
+  r0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
+  r1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
+}
+// 2^x of pair n of a run; with POLY of every 4 pairs by ex2_pair
+template <int POLY>
+__device__ __forceinline__ void ex2_of(int n, uint64_t x, float& r0, float& r1) {
+  if (n % 4 < POLY) {
+    ex2_pair(x, r0, r1);
+  } else {
+    unpack(x, r0, r1);
+    r0 = ex2_approx(r0);
+    r1 = ex2_approx(r1);
+  }
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -166,8 +225,18 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* s
                "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
                : "memory");
 }
+// Until this thread's TMA stores have read their shared memory.
 __device__ __forceinline__ void tma_store_wait() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+// Fetches a tile into L2 for a CTA to come.
+template <int HD>
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* m, int col, int row, int b) {
+#pragma unroll
+  for (int c = 0; c < HD / 64; ++c)
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(m)),
+                 "r"(col + c * 64), "r"(row), "r"(b)
+                 : "memory");
 }
 // D = A B^T over HD columns, A in TMEM (HD / 2 columns), B K-major in chunks of 64 columns
 template <int HD>
@@ -206,6 +275,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc bb, uint32_t
 // While a row's thread works on block j, the tensor cores form P V of j - 1 and S of j + 1.
 // The reference m of a row moves only when a block's maximum exceeds it by 2^8; O is then rescaled in
 // TMEM, once P V of j - 1 has been added. The tile of O leaves through Q's shared memory by TMA.
+// The query tile of CTA x: heads of a tile next to each other, the last tiles (the longest) first.
+struct QueryTile {
+  int h, b, q0;
+  __device__ __forceinline__ QueryTile(int x, int hq, int S) {
+    const int nq = (S + kQB - 1) / kQB, u = x / hq;
+    h = x % hq;
+    b = u / nq;
+    q0 = (nq - 1 - u % nq) * kQB;
+  }
+};
+
 template <int HD>
 struct FwdCfg {
   static constexpr int KB = 64;  // keys of a block
@@ -218,7 +298,8 @@ template <int HD>
 __global__ void __launch_bounds__(192, 2)
 k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmK16,
-             const __grid_constant__ CUtensorMap tmV16, const __grid_constant__ CUtensorMap tmO, const WinArgs p) {
+             const __grid_constant__ CUtensorMap tmV16, const __grid_constant__ CUtensorMap tmO, const WinArgs p,
+             const int ahead) {
   using C = FwdCfg<HD>;
   constexpr int kKB = C::KB;
   extern __shared__ uint8_t smem_raw[];
@@ -229,9 +310,8 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
            *v_empty = bars + 8, *s_full = bars + 10, *p_full = bars + 12;  // [2] from k_full on
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
 
-  const int nq = (p.S + kQB - 1) / kQB;
-  const int h = blockIdx.x % p.hq, u = blockIdx.x / p.hq;
-  const int b = u / nq, q0 = (nq - 1 - u % nq) * kQB;
+  const QueryTile tile(blockIdx.x, p.hq, p.S);
+  const int h = tile.h, b = tile.b, q0 = tile.q0;
   const int kvh = h / (p.hq / p.hkv);
   const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
   const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -265,6 +345,10 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     __syncwarp();
     bool ok = true;
     for (int j = 0; j < kb.n && ok; ++j) {
+      if (j == 2 && blockIdx.x + ahead < gridDim.x && elect_one()) {
+        const QueryTile next(blockIdx.x + ahead, p.hq, p.S);
+        prefetch_tile<HD>(&tmQ, next.h * HD, next.q0, next.b);
+      }
       const int k0 = kb.k0(j), w = kb.width(j), s = j & 1;
       for (int kv = 0; kv < 2; ++kv) {
         if (j >= 2 && !(ok = warp_wait((kv ? v_empty : k_empty) + s, ((j >> 1) - 1) & 1))) break;
@@ -309,8 +393,9 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     // the first NC columns of a block
-    const auto block = [&](auto nc, bool masked, int k0, int j) {
+    const auto block = [&](auto nc, auto mask, int k0, int j) {
       constexpr int NC = decltype(nc)::value;
+      constexpr bool masked = decltype(mask)::value;
       const uint32_t tX = tS + (j & 1) * kKB + lanes;
       float x[NC];
 #pragma unroll
@@ -325,8 +410,13 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       }
       float pm[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int c = 4; c < NC; ++c) pm[c & 3] = fmaxf(pm[c & 3], x[c]);
-      const float bm = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])) * sl2;
+      for (int c = 4; c < NC - 4; c += 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pm[e] = max3(pm[e], x[c + 2 * e], x[c + 2 * e + 1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pm[e] = fmaxf(pm[e], x[NC - 4 + e]);
+      const float bm = fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]) * sl2;
       float corr = 1.f;
       if (bm > m + 8.f) {
         corr = ex2_approx(m - bm);  // 0 where nothing was visible before
@@ -347,16 +437,19 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         }
       }
       const float mm = m > -INFINITY ? m : 0.f;  // a row that sees nothing so far
-      float ps[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t ps[2] = {0, 0};
       uint32_t w[NC / 2];
+      const uint64_t sl = f2(sl2, sl2), mn = f2(-mm, -mm);
 #pragma unroll
-      for (int c = 0; c < NC; c += 2) {
-        const float a0 = ex2_approx(fmaf(x[c], sl2, -mm)), a1 = ex2_approx(fmaf(x[c + 1], sl2, -mm));
-        ps[c & 3] += a0;
-        ps[(c + 1) & 3] += a1;
-        w[c / 2] = pack2(a0, a1);
+      for (int c = 0; c < NC / 2; ++c) {
+        float a0, a1;
+        ex2_of<masked ? 0 : 1>(c, fma2(f2(x[2 * c], x[2 * c + 1]), sl, mn), a0, a1);
+        ps[c & 1] = add2(ps[c & 1], f2(a0, a1));
+        w[c] = pack2(a0, a1);
       }
-      l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+      float l0, l1;
+      unpack(add2(ps[0], ps[1]), l0, l1);
+      l += l0 + l1;
 #pragma unroll
       for (int c = 0; c < NC / 2; c += 16) tmem_st16(tX + c, w + c);
       tmem_st_wait();
@@ -365,8 +458,12 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       if (!(ok = warp_wait(s_full + (j & 1), (j >> 1) & 1))) break;
       tc_fence_after();
       const int k0 = kb.k0(j);
-      if (kb.width(j) <= 32) block(std::integral_constant<int, 32>{}, true, k0, j);
-      else block(std::integral_constant<int, kKB>{}, !all_visible(q0, kQB, k0, kKB, p.window, p.sinks), k0, j);
+      if (all_visible(q0, kQB, k0, kKB, p.window, p.sinks))
+        block(std::integral_constant<int, kKB>{}, std::false_type{}, k0, j);
+      else if (kb.width(j) <= 32)
+        block(std::integral_constant<int, 32>{}, std::true_type{}, k0, j);
+      else
+        block(std::integral_constant<int, kKB>{}, std::true_type{}, k0, j);
       tc_fence_before();
       mbar_arrive(p_full + (j & 1));
     }
@@ -490,7 +587,7 @@ __global__ void __launch_bounds__(320, 1)
 k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
             const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
             const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16,
-            const __grid_constant__ CUtensorMap tmDq, const WinBwdArgs p) {
+            const __grid_constant__ CUtensorMap tmDq, const WinBwdArgs p, const int ahead) {
   using C = DqCfg<HD>;
   constexpr int NK = C::NK, NV = C::NV, kKB = C::KB;
   extern __shared__ uint8_t smem_raw[];
@@ -504,9 +601,8 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   float* sD = reinterpret_cast<float*>(bars + kBars + 1);  // [128]
 
-  const int nq = (p.S + kQB - 1) / kQB;
-  const int h = blockIdx.x % p.hq, u = blockIdx.x / p.hq;
-  const int b = u / nq, q0 = (nq - 1 - u % nq) * kQB;
+  const QueryTile tile(blockIdx.x, p.hq, p.S);
+  const int h = tile.h, b = tile.b, q0 = tile.q0;
   const int kvh = h / (p.hq / p.hkv);
   const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
   const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -543,6 +639,11 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     __syncwarp();
     bool ok = true;
     for (int j = 0; j < kb.n && ok; ++j) {
+      if (j == 1 && blockIdx.x + ahead < gridDim.x && elect_one()) {
+        const QueryTile next(blockIdx.x + ahead, p.hq, p.S);
+        prefetch_tile<HD>(&tmQ, next.h * HD, next.q0, next.b);
+        prefetch_tile<HD>(&tmO, next.h * HD, next.q0, next.b);
+      }
       const int k0 = kb.k0(j), w = kb.width(j);
       for (int kv = 0; kv < 2; ++kv) {
         const int ns = kv ? NV : NK, s = j % ns;
@@ -658,16 +759,28 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     asm volatile("bar.sync 1, 256;" ::: "memory");
     const float D = sD[r];
     p.D[stat_row(b, h, p.hq, p.S) + g * up(p.S, kQB) + i] = g ? D : lse2;
+    if (blockIdx.x + ahead < gridDim.x) {  // and the rows of o that a CTA to come forms its D from
+      const QueryTile next(blockIdx.x + ahead, p.hq, p.S);
+      const int64_t tt = (int64_t)next.b * p.S + next.q0 + r;
+      const char* src = p.o32 ? reinterpret_cast<const char*>(p.o32 + (tt * p.hq + next.h) * HD)
+                              : reinterpret_cast<const char*>(p.o + tt * p.ldo + (int64_t)next.h * HD);
+      const int bytes = HD * (p.o32 ? 4 : 2);
+      if (next.q0 + r < p.S)
+        for (int c = g * 128; c < bytes; c += 256) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
+    }
     const uint32_t tX = tS + g * 64 + lanes, tY = tP + g * 64 + lanes;
     // columns [64 g, 64 g + NC) of a block
-    const auto block = [&](auto nc, bool masked, int k0, int j) {
+    const uint64_t sl = f2(sl2, sl2), ln = f2(-lse2, -lse2), Dn = f2(-D, -D);
+    const auto block = [&](auto nc, auto mask, int k0, int j) {
       constexpr int NC = decltype(nc)::value;
+      constexpr bool masked = decltype(mask)::value;
       float x[NC], y[NC];
       tmem_row<NC>(x, tX);
       tc_fence_before();
       mbar_arrive(s_free);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) x[c] = ex2_approx(fmaf(x[c], sl2, -lse2));
+      for (int c = 0; c < NC / 2; ++c)
+        ex2_of<masked ? 0 : 2>(c, fma2(f2(x[2 * c], x[2 * c + 1]), sl, ln), x[2 * c], x[2 * c + 1]);
       if (masked) {
         const uint64_t vis = visible_keys(i, k0 + g * 64, p.window, p.sinks);
         const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
@@ -680,7 +793,11 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       tmem_row<NC>(y, tY);
       uint32_t w[NC / 2];
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) w[c] = pack2(x[2 * c] * (y[2 * c] - D), x[2 * c + 1] * (y[2 * c + 1] - D));
+      for (int c = 0; c < NC / 2; ++c) {
+        float d0, d1;
+        unpack(mul2(f2(x[2 * c], x[2 * c + 1]), add2(f2(y[2 * c], y[2 * c + 1]), Dn)), d0, d1);
+        w[c] = pack2(d0, d1);
+      }
 #pragma unroll
       for (int c = 0; c < NC / 2; c += 16) tmem_st16(tY + c, w + c);
       tmem_st_wait();
@@ -689,10 +806,12 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       if (!(ok = warp_wait(s_full, j & 1))) break;
       tc_fence_after();
       const int k0 = kb.k0(j);
-      if (kb.width(j) > 32) {
-        block(std::integral_constant<int, 64>{}, !all_visible(q0, kQB, k0, kKB, p.window, p.sinks), k0, j);
+      if (all_visible(q0, kQB, k0, kKB, p.window, p.sinks)) {
+        block(std::integral_constant<int, 64>{}, std::false_type{}, k0, j);
+      } else if (kb.width(j) > 32) {
+        block(std::integral_constant<int, 64>{}, std::true_type{}, k0, j);
       } else if (g == 0) {
-        block(std::integral_constant<int, 32>{}, true, k0, j);
+        block(std::integral_constant<int, 32>{}, std::true_type{}, k0, j);
       } else {
         mbar_arrive(s_free);
         ok = warp_wait(dp_full, j & 1);
@@ -882,7 +1001,7 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     const int r = (warp & 3) * 32 + lane, key = k0 + r;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tX = tS + half * 64 + lanes, tY = tP + half * 64 + lanes;
-    const float sl2 = p.scale * kLog2e;
+    const uint64_t sl = f2(p.scale * kLog2e, p.scale * kLog2e);
     bool ok = true;
     for (int j = 0; j < n && ok; ++j) {
       const int q = query(j);
@@ -894,17 +1013,22 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       float x[64], y[64];
       uint32_t w[32];
       tmem_row<64>(x, tX);
+      if (all_visible(q, C::QB, k0, kQB, p.window, p.sinks)) {
 #pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        const float4 l4 = lse[c / 4];
-        x[c] = ex2_approx(fmaf(x[c], sl2, -l4.x));
-        x[c + 1] = ex2_approx(fmaf(x[c + 1], sl2, -l4.y));
-        x[c + 2] = ex2_approx(fmaf(x[c + 2], sl2, -l4.z));
-        x[c + 3] = ex2_approx(fmaf(x[c + 3], sl2, -l4.w));
-      }
-      if (!all_visible(q, C::QB, k0, kQB, p.window, p.sinks)) {
+        for (int c = 0; c < 64; c += 4) {
+          const float4 l4 = lse[c / 4];
+          ex2_of<2>(c / 2, fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
+          ex2_of<2>(c / 2 + 1, fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
+        }
+      } else {
         const uint64_t vis = visible_queries(key, q + half * 64, p.window, p.sinks);
         const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 l4 = lse[c / 4];
+          ex2_of<0>(c / 2, fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
+          ex2_of<0>(c / 2 + 1, fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
+        }
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           if (!(bits[c / 32] >> (c % 32) & 1)) x[c] = 0.f;
@@ -922,8 +1046,11 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
       for (int c = 0; c < 64; c += 4) {
         const float4 d4 = del[c / 4];
-        w[c / 2] = pack2(x[c] * (y[c] - d4.x), x[c + 1] * (y[c + 1] - d4.y));
-        w[c / 2 + 1] = pack2(x[c + 2] * (y[c + 2] - d4.z), x[c + 3] * (y[c + 3] - d4.w));
+        float a0, a1, a2, a3;
+        unpack(mul2(f2(x[c], x[c + 1]), add2(f2(y[c], y[c + 1]), f2(-d4.x, -d4.y))), a0, a1);
+        unpack(mul2(f2(x[c + 2], x[c + 3]), add2(f2(y[c + 2], y[c + 3]), f2(-d4.z, -d4.w))), a2, a3);
+        w[c / 2] = pack2(a0, a1);
+        w[c / 2 + 1] = pack2(a2, a3);
       }
       tmem_st16(tY, w);
       tmem_st16(tY + 16, w + 16);
@@ -1089,7 +1216,8 @@ cudaError_t launch_fwd(const WinArgs& a, cudaStream_t s) {
   const cudaError_t e = allow_smem(k_window_fwd<HD>, C::SMEM, done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = B * a.hq * ((a.S + kQB - 1) / kQB);
-  return launch_k(k_window_fwd<HD>, dim3((unsigned)tiles), dim3(192), C::SMEM, s, 0, q, k, v, k16, v16, o, a);
+  return launch_k(k_window_fwd<HD>, dim3((unsigned)tiles), dim3(192), C::SMEM, s, 0, q, k, v, k16, v16, o, a,
+                  2 * device_sm_count());
 }
 
 template <int HD>
@@ -1109,7 +1237,8 @@ cudaError_t launch_bwd(const WinBwdArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = allow_smem(k_window_dkdv<HD>, K::SMEM, done_k);
   if (e != cudaSuccess) return e;
   const int64_t tiles = B * a.hq * ((a.S + kQB - 1) / kQB);
-  e = launch_k(k_window_dq<HD>, dim3((unsigned)tiles), dim3(320), Q::SMEM, s, 0, q, o, k, v, k16, v16, dq, a);
+  e = launch_k(k_window_dq<HD>, dim3((unsigned)tiles), dim3(320), Q::SMEM, s, 0, q, o, k, v, k16, v16, dq, a,
+               device_sm_count());
   note_launch(1);
   if (e != cudaSuccess) return e;
   const Split sp = plan_split(a.T, a.S, a.hq, a.hkv, a.window, a.sinks);
