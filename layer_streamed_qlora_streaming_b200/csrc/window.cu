@@ -152,6 +152,19 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// Barrier of `threads` threads (whole warps); true for all of them when ok holds for all.
+__device__ __forceinline__ bool sync_all(int id, int threads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
 // Wait of a whole warp; false (for all of it) once it ran out.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -513,31 +526,37 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 // 0 or 1: x * scale with the rotary embedding of position pos undone, as bf16 into the row's place of a
 // swizzled tile (chunks of 64 columns).
 template <int HD>
-__device__ __forceinline__ void stage_grad(uint8_t* tile, uint32_t chunk, int row, const float (&lo)[HD / 4],
-                                           const float (&hi)[HD / 4], const AttnBwdArgs& p, int pos, int part) {
+__device__ __forceinline__ void stage_grad(uint8_t* tile, uint32_t chunk, int row, float (&lo)[HD / 4], float (&hi)[HD / 4],
+                                           const AttnBwdArgs& p, int pos, int part) {
   constexpr int HALF = HD / 2, Q4 = HD / 4;
-  const bool rope = p.rope_cos && pos < p.S;
 #pragma unroll
-  for (int c0 = 0; c0 < Q4; c0 += 8) {
-    const int c = part * Q4 + c0;
-    float y1[8], y2[8];
+  for (int e = 0; e < Q4; ++e) {
+    lo[e] *= p.scale;
+    hi[e] *= p.scale;
+  }
+  if (p.rope_cos && pos < p.S) {
+    const float4* ct = reinterpret_cast<const float4*>(p.rope_cos + (int64_t)pos * HALF + part * Q4);
+    const float4* st = reinterpret_cast<const float4*>(p.rope_sin + (int64_t)pos * HALF + part * Q4);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y1[e] = lo[c0 + e] * p.scale;
-      y2[e] = hi[c0 + e] * p.scale;
-      if (rope) {
-        const float cs = p.rope_cos[(int64_t)pos * HALF + c + e], sn = p.rope_sin[(int64_t)pos * HALF + c + e];
-        const float a = y1[e] * cs + y2[e] * sn;
-        y2[e] = y2[e] * cs - y1[e] * sn;
-        y1[e] = a;
+    for (int e = 0; e < Q4; e += 4) {
+      const float4 c4 = ct[e / 4], s4 = st[e / 4];
+      const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float a = lo[e + u] * cs[u] + hi[e + u] * sn[u];
+        hi[e + u] = hi[e + u] * cs[u] - lo[e + u] * sn[u];
+        lo[e + u] = a;
       }
     }
-    const auto put = [&](int col, const float* y) {
-      *reinterpret_cast<uint4*>(tile + col / 64 * chunk + row * 128 + ((col % 64 / 8) ^ (row & 7)) * 16) =
-          make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
-    };
-    put(c, y1);
-    put(c + HALF, y2);
+  }
+  const auto put = [&](int col, const float* y) {
+    *reinterpret_cast<uint4*>(tile + col / 64 * chunk + row * 128 + ((col % 64 / 8) ^ (row & 7)) * 16) =
+        make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+  };
+#pragma unroll
+  for (int e = 0; e < Q4; e += 8) {
+    put(part * Q4 + e, lo + e);
+    put(part * Q4 + e + HALF, hi + e);
   }
 }
 // N consecutive TMEM columns of this thread's row
@@ -565,46 +584,44 @@ __host__ __device__ __forceinline__ int64_t stat_row(int b, int h, int hq, int S
 }
 
 // ---------------------------------------------------------------------------------- dQ
-// One CTA per query tile of one head, 320 threads: warp 0 TMA (three K and two V blocks of 128 keys in
-// flight), warp 1 the MMAs, warps 2-9 two threads a query row (half of a block's columns each).
+// Persistent CTAs, one an SM, taking the query tiles in turn; 320 threads: warp 0 TMA (the next tile's Q and
+// dO, two K and two V blocks of 128 keys in flight), warp 1 the MMAs, warps 2-9 two threads a query row
+// (half of a block's columns each).
 // Q and dO are copied into TMEM first and serve as the A operands from there: read from shared memory for
 // every block they took its whole bandwidth (128 bytes a clock: with K, V, their loads and dS K 1800
-// clocks a block, where the tensor cores take 1540). S of block j + 1 is issued as soon as the threads
-// have read S of j; dS goes over dP (bf16, the A operand of dQ += dS K), and dP of j + 1 follows that
-// product, under the exponentials of j + 1. (Blocks of 64 keys with two buffers of each took 2060 clocks
-// a block: at N = 64 the issue of an MMA takes longer than its 32 clocks.)
+// clocks a block, where the tensor cores take 1540), and their place is free for the next tile's.
+// S of block j + 1 is issued as soon as the threads have read S of j; dS goes over dP (bf16, the A operand
+// of dQ += dS K), and dP of j + 1 follows that product, under the exponentials of j + 1. (Blocks of 64 keys
+// with two buffers of each took 2060 clocks a block: at N = 64 the issue of an MMA takes longer than its
+// 32 clocks.) The tile of dQ leaves by TMA under the next tile. With a CTA a tile, its start (setup, Q,
+// dO, o) and end took 9500 clocks of the 31600 of a tile of ten blocks.
 template <int HD>
 struct DqCfg {
   static constexpr int KB = 128;  // keys of a block
   static constexpr uint32_t CH = kQB * 128;
   static constexpr uint32_t TILE = (HD / 64) * CH;
-  static constexpr int NK = 3, NV = 2;
-  static constexpr uint32_t SMEM = (2 + NK + NV) * TILE + 1024 + 256 + kQB * 4;
+  static constexpr uint32_t SMEM = 7 * TILE + 1024 + 256 + kQB * 4;
 };
 
-template <int HD>
+template <int HD, bool O32>
 __global__ void __launch_bounds__(320, 1)
 k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
             const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
             const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16,
-            const __grid_constant__ CUtensorMap tmDq, const WinBwdArgs p, const int ahead) {
+            const __grid_constant__ CUtensorMap tmDq, const WinBwdArgs p, const int tiles) {
   using C = DqCfg<HD>;
-  constexpr int NK = C::NK, NV = C::NV, kKB = C::KB;
+  constexpr int kKB = C::KB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sQ = smem, *sO = smem + C::TILE, *sK = smem + 2 * C::TILE, *sV = sK + NK * C::TILE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + NV * C::TILE);
+  uint8_t *sQ = smem, *sO = smem + C::TILE, *sK = smem + 2 * C::TILE, *sV = smem + 4 * C::TILE, *sG = smem + 6 * C::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 7 * C::TILE);
   uint64_t *a_full = bars, *s_free = bars + 1, *ds_full = bars + 2;  // of all 256 row threads
   uint64_t *q_full = bars + 3, *s_full = bars + 4, *dp_full = bars + 5, *done = bars + 6;
-  uint64_t *k_full = bars + 7, *k_empty = k_full + NK, *v_full = k_empty + NK, *v_empty = v_full + NV;
-  constexpr int kBars = 7 + 2 * NK + 2 * NV;
+  uint64_t *k_full = bars + 7, *k_empty = bars + 9, *v_full = bars + 11, *v_empty = bars + 13;  // [2]
+  constexpr int kBars = 15;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   float* sD = reinterpret_cast<float*>(bars + kBars + 1);  // [128]
-
-  const QueryTile tile(blockIdx.x, p.hq, p.S);
-  const int h = tile.h, b = tile.b, q0 = tile.q0;
-  const int kvh = h / (p.hq / p.hkv);
-  const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
+  const int grp = p.hq / p.hkv;
   const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -630,210 +647,217 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   pdl_wait();
   pdl_trigger();
 
+  // it counts the CTA's tiles, jj its blocks: barrier phases run on over the tiles
   if (warp == 0) {
-    if (elect_one()) {
-      mbar_arrive_expect_tx(q_full, 2 * C::TILE);
-      load_tile<HD>(sQ, C::CH, &tmQ, q_full, h * HD, q0, b);
-      load_tile<HD>(sO, C::CH, &tmO, q_full, h * HD, q0, b);
-    }
-    __syncwarp();
     bool ok = true;
-    for (int j = 0; j < kb.n && ok; ++j) {
-      if (j == 1 && blockIdx.x + ahead < gridDim.x && elect_one()) {
-        const QueryTile next(blockIdx.x + ahead, p.hq, p.S);
-        prefetch_tile<HD>(&tmQ, next.h * HD, next.q0, next.b);
-        prefetch_tile<HD>(&tmO, next.h * HD, next.q0, next.b);
+    int it = 0, jj = 0;
+    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it) {
+      const QueryTile tile(x, p.hq, p.S);
+      const Blocks<kKB> kb(tile.q0, p.S, p.window, p.sinks);
+      const int kvh = tile.h / grp;
+      if (it > 0 && !(ok = warp_wait(a_full, (it - 1) & 1))) break;  // the last tile's Q and dO have been copied
+      if (elect_one()) {
+        mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+        load_tile<HD>(sQ, C::CH, &tmQ, q_full, tile.h * HD, tile.q0, tile.b);
+        load_tile<HD>(sO, C::CH, &tmO, q_full, tile.h * HD, tile.q0, tile.b);
       }
-      const int k0 = kb.k0(j), w = kb.width(j);
-      for (int kv = 0; kv < 2; ++kv) {
-        const int ns = kv ? NV : NK, s = j % ns;
-        if (j >= ns && !(ok = warp_wait((kv ? v_empty : k_empty) + s, (j / ns - 1) & 1))) break;
-        if (elect_one())
-          load_keys<HD, kKB>((kv ? sV : sK) + s * C::TILE, C::CH, kv ? &tmV : &tmK, kv ? &tmV16 : &tmK16,
-                             (kv ? v_full : k_full) + s, kvh * HD, k0, w, b);
-        __syncwarp();
+      __syncwarp();
+      for (int j = 0; j < kb.n && ok; ++j, ++jj) {
+        const int k0 = kb.k0(j), w = kb.width(j), s = jj & 1;
+        for (int kv = 0; kv < 2; ++kv) {
+          if (jj >= 2 && !(ok = warp_wait((kv ? v_empty : k_empty) + s, ((jj >> 1) - 1) & 1))) break;
+          if (elect_one())
+            load_keys<HD, kKB>((kv ? sV : sK) + s * C::TILE, C::CH, kv ? &tmV : &tmK, kv ? &tmV16 : &tmK16,
+                               (kv ? v_full : k_full) + s, kvh * HD, k0, w, tile.b);
+          __syncwarp();
+        }
       }
     }
   } else if (warp == 1) {
     constexpr uint32_t idQ = umma_idesc_bf16(128, HD, 0, 1);
-    bool ok = warp_wait(a_full, 0);
-    const auto scores = [&](int j) {  // S_j = Q K_j^T
-      const int s = j % NK;
-      if (!(ok = ok && warp_wait(k_full + s, (j / NK) & 1))) return;
+    bool ok = true;
+    const auto scores = [&](int jj, int w) {  // S = Q K^T
+      if (!(ok = ok && warp_wait(k_full + (jj & 1), (jj >> 1) & 1))) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_tt<HD>(tS, tA, make_desc(smem_u32(sK + s * C::TILE), 16, 1024), C::CH, umma_idesc_bf16(128, kb.width(j), 0, 0));
+        mma_tt<HD>(tS, tA, make_desc(smem_u32(sK + (jj & 1) * C::TILE), 16, 1024), C::CH, umma_idesc_bf16(128, w, 0, 0));
         umma_commit(s_full);
       }
       __syncwarp();
     };
-    const auto dprobs = [&](int j) {  // dP_j = dO V_j^T
-      const int s = j % NV;
-      if (!(ok = ok && warp_wait(v_full + s, (j / NV) & 1))) return;
+    const auto dprobs = [&](int jj, int w) {  // dP = dO V^T
+      if (!(ok = ok && warp_wait(v_full + (jj & 1), (jj >> 1) & 1))) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_tt<HD>(tP, tA + 64, make_desc(smem_u32(sV + s * C::TILE), 16, 1024), C::CH,
-                   umma_idesc_bf16(128, kb.width(j), 0, 0));
+        mma_tt<HD>(tP, tA + 64, make_desc(smem_u32(sV + (jj & 1) * C::TILE), 16, 1024), C::CH, umma_idesc_bf16(128, w, 0, 0));
         umma_commit(dp_full);
-        umma_commit(v_empty + s);
+        umma_commit(v_empty + (jj & 1));
       }
       __syncwarp();
     };
-    scores(0);
-    dprobs(0);
-    for (int j = 0; j < kb.n && ok; ++j) {
-      if (j + 1 < kb.n) {
-        if (!(ok = warp_wait(s_free, j & 1))) break;
-        scores(j + 1);
+    int it = 0, jj = 0;
+    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it) {
+      const QueryTile tile(x, p.hq, p.S);
+      const Blocks<kKB> kb(tile.q0, p.S, p.window, p.sinks);
+      if (!(ok = warp_wait(a_full, it & 1))) break;
+      scores(jj, kb.width(0));
+      dprobs(jj, kb.width(0));
+      for (int j = 0; j < kb.n && ok; ++j, ++jj) {
+        const int next = j + 1 < kb.n ? kb.width(j + 1) : 0;
+        if (next) {
+          if (!(ok = warp_wait(s_free, jj & 1))) break;
+          scores(jj + 1, next);
+        }
+        // dS is written; with a tile's first block its threads have also read the last tile's dQ
+        if (!(ok = ok && warp_wait(ds_full, jj & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {  // each half of a block's columns holds its own 64 keys' dS
+          mma_ts<kKB, 64>(tQ, tP, make_desc(smem_u32(sK + (jj & 1) * C::TILE), C::CH, 1024), idQ, kb.width(j), j > 0);
+          umma_commit(k_empty + (jj & 1));
+          if (!next) umma_commit(done);
+        }
+        __syncwarp();
+        if (next) dprobs(jj + 1, next);
       }
-      if (!(ok = ok && warp_wait(ds_full, j & 1))) break;
-      tc_fence_after();
-      if (elect_one()) {  // each half of a block's columns holds its own 64 keys' dS
-        mma_ts<kKB, 64>(tQ, tP, make_desc(smem_u32(sK + j % NK * C::TILE), C::CH, 1024), idQ, kb.width(j), j > 0);
-        umma_commit(j + 1 < kb.n ? k_empty + j % NK : done);
-      }
-      __syncwarp();
-      if (j + 1 < kb.n) dprobs(j + 1);
     }
   } else {
     const int g = (int)(threadIdx.x - 64) >> 7;  // half of the columns
-    const int r = (warp & 3) * 32 + lane, i = q0 + r;
+    const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const bool live = i < p.S;
-    const int64_t t = (int64_t)b * p.S + i;
+    const uint32_t tX = tS + g * 64 + lanes, tY = tP + g * 64 + lanes;
     const float sl2 = p.scale * kLog2e;
-    const float lse2 = live ? p.lse[t * p.hq + h] * kLog2e : INFINITY;
-    // D of the tile's rows, from the forward's unrounded o where it was kept: a warp takes 16 rows, HD / 8
-    // lanes a row, every load in flight before the first sum
-    {
-      constexpr int LPR = HD / 8, RPI = 32 / LPR;  // lanes a row, rows a load
-      const int w8 = warp - 2, col = lane % LPR * 8;
-      uint4 dv[16 / RPI];
-      float4 ov[16 / RPI][2];
+    const uint64_t sl = f2(sl2, sl2);
+    bool ok = true;
+    // D of a tile's rows, from the forward's unrounded o where it was kept: a warp takes 16 rows, HD / 8 lanes
+    // a row; o is fetched ahead
+    constexpr int LPR = HD / 8, RPI = 32 / LPR, ROWS = 16 / RPI;  // lanes a row, rows a load, loads
+    const int drow = (warp - 2) * 16 + lane / LPR, dcol = lane % LPR * 8;
+    uint4 ov[ROWS][O32 ? 2 : 1];
+    const auto fetch_o = [&](int x) {
+      if (x >= tiles) return;
+      const QueryTile t(x, p.hq, p.S);
 #pragma unroll
-      for (int n = 0; n < 16 / RPI; ++n) {
-        const int row = q0 + w8 * 16 + n * RPI + lane / LPR;
-        const int64_t tt = (int64_t)b * p.S + row;
-        dv[n] = make_uint4(0, 0, 0, 0);
-        ov[n][0] = ov[n][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < p.S) {
-          dv[n] = *reinterpret_cast<const uint4*>(p.dout + tt * p.lddo + (int64_t)h * HD + col);
-          if (p.o32) {
-            const float4* src = reinterpret_cast<const float4*>(p.o32 + (tt * p.hq + h) * HD + col);
-            ov[n][0] = src[0];
-            ov[n][1] = src[1];
-          } else {
-            *reinterpret_cast<uint4*>(&ov[n][0]) = *reinterpret_cast<const uint4*>(p.o + tt * p.ldo + (int64_t)h * HD + col);
-          }
+      for (int n = 0; n < ROWS; ++n) {
+        const int row = t.q0 + drow + n * RPI;
+        const int64_t tt = (int64_t)t.b * p.S + row;
+#pragma unroll
+        for (int e = 0; e < (O32 ? 2 : 1); ++e) {
+          ov[n][e] = make_uint4(0, 0, 0, 0);
+          if (row < p.S)
+            ov[n][e] = O32 ? *reinterpret_cast<const uint4*>(p.o32 + (tt * p.hq + t.h) * HD + dcol + 4 * e)
+                           : *reinterpret_cast<const uint4*>(p.o + tt * p.ldo + (int64_t)t.h * HD + dcol);
         }
       }
+    };
+    fetch_o(blockIdx.x);
+    int it = 0, jj = 0;
+    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it) {
+      const QueryTile tile(x, p.hq, p.S);
+      const int q0 = tile.q0, i = q0 + r;
+      const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
+      const int64_t t = (int64_t)tile.b * p.S + i;
+      const float lse2 = i < p.S ? p.lse[t * p.hq + tile.h] * kLog2e : INFINITY;
+      // a wait that runs out is shared at the next barrier, which every warp reaches
+      ok = warp_wait(q_full, it & 1);
 #pragma unroll
-      for (int n = 0; n < 16 / RPI; ++n) {
-        const __nv_bfloat16* d8 = reinterpret_cast<const __nv_bfloat16*>(&dv[n]);
+      for (int n = 0; n < ROWS; ++n) {
+        const int row = drow + n * RPI;
+        const uint4 dv = *reinterpret_cast<const uint4*>(sO + dcol / 64 * C::CH + row * 128 + ((dcol % 64 / 8) ^ (row & 7)) * 16);
+        const __nv_bfloat16* d8 = reinterpret_cast<const __nv_bfloat16*>(&dv);
         const __nv_bfloat16* o8 = reinterpret_cast<const __nv_bfloat16*>(&ov[n][0]);
         const float* f8 = reinterpret_cast<const float*>(&ov[n][0]);
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += __bfloat162float(d8[e]) * (p.o32 ? f8[e] : __bfloat162float(o8[e]));
+        for (int e = 0; e < 8; ++e) sum += __bfloat162float(d8[e]) * (O32 ? f8[e] : __bfloat162float(o8[e]));
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane % LPR == 0) sD[w8 * 16 + n * RPI + lane / LPR] = sum;
+        if (lane % LPR == 0) sD[row] = sum;
       }
-    }
-    // the first four warps copy Q's rows into TMEM, the others dO's
-    bool ok = warp_wait(q_full, 0);
-    if (ok) {
-      const uint8_t* src = g ? sO : sQ;
+      {  // the first four warps copy Q's rows into TMEM, the others dO's
+        const uint8_t* src = g ? sO : sQ;
 #pragma unroll
-      for (int c = 0; c < HD / 64; ++c) {
-        uint32_t w[32];
+        for (int c = 0; c < HD / 64; ++c) {
+          uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(w + 4 * e) = *reinterpret_cast<const uint4*>(src + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
-        tmem_st32(tA + g * 64 + c * 32 + lanes, w);
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(w + 4 * e) = *reinterpret_cast<const uint4*>(src + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
+          tmem_st32(tA + g * 64 + c * 32 + lanes, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(a_full);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(a_full);
-    }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    const float D = sD[r];
-    p.D[stat_row(b, h, p.hq, p.S) + g * up(p.S, kQB) + i] = g ? D : lse2;
-    if (blockIdx.x + ahead < gridDim.x) {  // and the rows of o that a CTA to come forms its D from
-      const QueryTile next(blockIdx.x + ahead, p.hq, p.S);
-      const int64_t tt = (int64_t)next.b * p.S + next.q0 + r;
-      const char* src = p.o32 ? reinterpret_cast<const char*>(p.o32 + (tt * p.hq + next.h) * HD)
-                              : reinterpret_cast<const char*>(p.o + tt * p.ldo + (int64_t)next.h * HD);
-      const int bytes = HD * (p.o32 ? 4 : 2);
-      if (next.q0 + r < p.S)
-        for (int c = g * 128; c < bytes; c += 256) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
-    }
-    const uint32_t tX = tS + g * 64 + lanes, tY = tP + g * 64 + lanes;
-    // columns [64 g, 64 g + NC) of a block
-    const uint64_t sl = f2(sl2, sl2), ln = f2(-lse2, -lse2), Dn = f2(-D, -D);
-    const auto block = [&](auto nc, auto mask, int k0, int j) {
-      constexpr int NC = decltype(nc)::value;
-      constexpr bool masked = decltype(mask)::value;
-      float x[NC], y[NC];
-      tmem_row<NC>(x, tX);
-      tc_fence_before();
-      mbar_arrive(s_free);
-#pragma unroll
-      for (int c = 0; c < NC / 2; ++c)
-        ex2_of<masked ? 0 : 2>(c, fma2(f2(x[2 * c], x[2 * c + 1]), sl, ln), x[2 * c], x[2 * c + 1]);
-      if (masked) {
-        const uint64_t vis = visible_keys(i, k0 + g * 64, p.window, p.sinks);
-        const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-          if (!(bits[c / 32] >> (c % 32) & 1)) x[c] = 0.f;
-      }
-      if (!(ok = warp_wait(dp_full, j & 1))) return;
-      tc_fence_after();
-      tmem_row<NC>(y, tY);
-      uint32_t w[NC / 2];
-#pragma unroll
-      for (int c = 0; c < NC / 2; ++c) {
-        float d0, d1;
-        unpack(mul2(f2(x[2 * c], x[2 * c + 1]), add2(f2(y[2 * c], y[2 * c + 1]), Dn)), d0, d1);
-        w[c] = pack2(d0, d1);
-      }
-#pragma unroll
-      for (int c = 0; c < NC / 2; c += 16) tmem_st16(tY + c, w + c);
-      tmem_st_wait();
-    };
-    for (int j = 0; j < kb.n && ok; ++j) {
-      if (!(ok = warp_wait(s_full, j & 1))) break;
-      tc_fence_after();
-      const int k0 = kb.k0(j);
-      if (all_visible(q0, kQB, k0, kKB, p.window, p.sinks)) {
-        block(std::integral_constant<int, 64>{}, std::false_type{}, k0, j);
-      } else if (kb.width(j) > 32) {
-        block(std::integral_constant<int, 64>{}, std::true_type{}, k0, j);
-      } else if (g == 0) {
-        block(std::integral_constant<int, 32>{}, std::true_type{}, k0, j);
-      } else {
+      if (warp == 2) tma_store_wait();  // the last tile's dQ has left sG
+      if (!(ok = sync_all(1, 256, ok))) break;
+      const float D = sD[r];
+      const uint64_t ln = f2(-lse2, -lse2), Dn = f2(-D, -D);
+      p.D[stat_row(tile.b, tile.h, p.hq, p.S) + g * up(p.S, kQB) + i] = g ? D : lse2;
+      // columns [64 g, 64 g + NC) of a block
+      const auto block = [&](auto nc, auto mask, int k0) {
+        constexpr int NC = decltype(nc)::value;
+        constexpr bool masked = decltype(mask)::value;
+        float a[NC], y[NC];
+        tmem_row<NC>(a, tX);
+        tc_fence_before();
         mbar_arrive(s_free);
-        ok = warp_wait(dp_full, j & 1);
-      }
-      tc_fence_before();
-      mbar_arrive(ds_full);
-    }
-    ok = ok && warp_wait(done, 0);
-    if (ok) {  // Q's shared memory takes the tile of dQ
-      tc_fence_after();
-      float lo[HD / 4], hi[HD / 4];
-      tmem_row<HD / 4>(lo, tQ + g * (HD / 4) + lanes);
-      tmem_row<HD / 4>(hi, tQ + g * (HD / 4) + HD / 2 + lanes);
-      stage_grad<HD>(sQ, C::CH, r, lo, hi, p, i, g);
-      fence_proxy_async();
-    }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (warp == 2 && ok && elect_one()) {
 #pragma unroll
-      for (int c = 0; c < HD / 64; ++c) tma_store_3d(&tmDq, sQ + c * C::CH, h * HD + c * 64, q0, b);
-      tma_store_wait();
+        for (int c = 0; c < NC / 2; ++c)
+          ex2_of<masked ? 0 : 2>(c, fma2(f2(a[2 * c], a[2 * c + 1]), sl, ln), a[2 * c], a[2 * c + 1]);
+        if (masked) {
+          const uint64_t vis = visible_keys(i, k0 + g * 64, p.window, p.sinks);
+          const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            if (!(bits[c / 32] >> (c % 32) & 1)) a[c] = 0.f;
+        }
+        if (!(ok = warp_wait(dp_full, jj & 1))) return;
+        tc_fence_after();
+        tmem_row<NC>(y, tY);
+        uint32_t w[NC / 2];
+#pragma unroll
+        for (int c = 0; c < NC / 2; ++c) {
+          float d0, d1;
+          unpack(mul2(f2(a[2 * c], a[2 * c + 1]), add2(f2(y[2 * c], y[2 * c + 1]), Dn)), d0, d1);
+          w[c] = pack2(d0, d1);
+        }
+#pragma unroll
+        for (int c = 0; c < NC / 2; c += 16) tmem_st16(tY + c, w + c);
+        tmem_st_wait();
+      };
+      for (int j = 0; j < kb.n && ok; ++j, ++jj) {
+        if (!(ok = warp_wait(s_full, jj & 1))) break;
+        tc_fence_after();
+        const int k0 = kb.k0(j);
+        if (all_visible(q0, kQB, k0, kKB, p.window, p.sinks)) {
+          block(std::integral_constant<int, 64>{}, std::false_type{}, k0);
+        } else if (kb.width(j) > 32) {
+          block(std::integral_constant<int, 64>{}, std::true_type{}, k0);
+        } else if (g == 0) {
+          block(std::integral_constant<int, 32>{}, std::true_type{}, k0);
+        } else {
+          mbar_arrive(s_free);
+          ok = warp_wait(dp_full, jj & 1);
+        }
+        tc_fence_before();
+        mbar_arrive(ds_full);
+      }
+      fetch_o(x + gridDim.x);
+      if ((ok = ok && warp_wait(done, it & 1))) {
+        tc_fence_after();
+        float lo[HD / 4], hi[HD / 4];
+        tmem_row<HD / 4>(lo, tQ + g * (HD / 4) + lanes);
+        tmem_row<HD / 4>(hi, tQ + g * (HD / 4) + HD / 2 + lanes);
+        stage_grad<HD>(sG, C::CH, r, lo, hi, p, i, g);
+        fence_proxy_async();
+      }
+      if (!(ok = sync_all(1, 256, ok))) break;
+      if (warp == 2 && elect_one()) {
+#pragma unroll
+        for (int c = 0; c < HD / 64; ++c) tma_store_3d(&tmDq, sG + c * C::CH, tile.h * HD + c * 64, q0, tile.b);
+      }
+      __syncwarp();
     }
+    if (warp == 2) tma_store_wait();
   }
   __syncwarp();
   tc_fence_before();
@@ -1232,13 +1256,14 @@ cudaError_t launch_bwd(const WinBwdArgs& a, cudaStream_t s) {
       !make_map3(&dq, a.dq, B, a.S, cq, a.lddq, kQB) || !make_map3(&dk, a.dk, B, a.S, ck, a.lddk, kQB) ||
       !make_map3(&dv, a.dv, B, a.S, ck, a.lddv, kQB))
     return cudaErrorInvalidValue;
-  static std::atomic<unsigned long long> done_q{0}, done_k{0};
-  cudaError_t e = allow_smem(k_window_dq<HD>, Q::SMEM, done_q);
+  static std::atomic<unsigned long long> done_q{0}, done_q32{0}, done_k{0};
+  const auto dq_kernel = a.o32 ? k_window_dq<HD, true> : k_window_dq<HD, false>;
+  cudaError_t e = allow_smem(dq_kernel, Q::SMEM, a.o32 ? done_q32 : done_q);
   if (e == cudaSuccess) e = allow_smem(k_window_dkdv<HD>, K::SMEM, done_k);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = B * a.hq * ((a.S + kQB - 1) / kQB);
-  e = launch_k(k_window_dq<HD>, dim3((unsigned)tiles), dim3(320), Q::SMEM, s, 0, q, o, k, v, k16, v16, dq, a,
-               device_sm_count());
+  const int tiles = (int)(B * a.hq * ((a.S + kQB - 1) / kQB));
+  e = launch_k(dq_kernel, dim3((unsigned)std::min(tiles, device_sm_count())), dim3(320), Q::SMEM, s, 0, q, o, k, v, k16,
+               v16, dq, a, tiles);
   note_launch(1);
   if (e != cudaSuccess) return e;
   const Split sp = plan_split(a.T, a.S, a.hq, a.hkv, a.window, a.sinks);
