@@ -20,7 +20,6 @@
 
 #include <algorithm>
 #include <cudaTypedefs.h>
-#include <type_traits>
 
 namespace lst {
 
@@ -60,24 +59,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 // 2^x of a pair on the FMA pipe: x = n + f with n the nearest whole number (by adding 1.5 * 2^23, whose low
 // bits then hold n), 2^f on [-1/2, 1/2] by the polynomial of degree 4 of least relative error (2.7e-6, by
-// Remez' exchange), n added to its exponent. x up to 120; what lies below -125 counts as -125. The
+// Remez' exchange), n added to its exponent. For x up to 120; 0 below -125 and for -infinity. The
 // exponential unit gives 16 values a clock and SM, so a tile of 128 x 128 takes it 1024 clocks, as long as
 // two of its matrix products: a share of the pairs goes this way.
 __device__ __forceinline__ void ex2_pair(uint64_t x, float& r0, float& r1) {
   constexpr float kMagic = 12582912.f;
-  float x0, x1;
-  unpack(x, x0, x1);
-  x = f2(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
-  const uint64_t t = add2(x, f2(kMagic, kMagic)), f = add2(x, mul2(add2(t, f2(-kMagic, -kMagic)), f2(-1.f, -1.f)));
+  const uint64_t t = add2(x, f2(kMagic, kMagic)), f = fma2(add2(t, f2(-kMagic, -kMagic)), f2(-1.f, -1.f), x);
   uint64_t q = fma2(f, f2(0.009570102f, 0.009570102f), f2(0.05591786f, 0.05591786f));
   q = fma2(q, f, f2(0.24024744f, 0.24024744f));
   q = fma2(q, f, f2(0.6931218f, 0.6931218f));
   q = fma2(q, f, f2(0.9999993f, 0.9999993f));
-  float t0, t1, q0, q1;
+  float x0, x1, t0, t1, q0, q1;
+  unpack(x, x0, x1);
   unpack(t, t0, t1);
   unpack(q, q0, q1);
-  r0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
-  r1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
+  r0 = x0 < -125.f ? 0.f : __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
+  r1 = x1 < -125.f ? 0.f : __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
 }
 // 2^x of pair n of a run; with POLY of every 4 pairs by ex2_pair
 template <int POLY>
@@ -165,9 +162,14 @@ __device__ __forceinline__ bool sync_all(int id, int threads, bool ok) {
       : "memory");
   return r != 0;
 }
-// Wait of a whole warp; false (for all of it) once it ran out.
+// Wait of a whole warp; false (for all of it) once it ran out. Not unrolled: there are many of them, and the
+// kernels' code has to stay in the instruction cache (dQ with 111 KB of code took 3000 clocks a block).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  bool done = false;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kSpinLimit && !done; ++i) done = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+  if (!done) dev_fail(DEV_ERR_MBAR_TIMEOUT);
+  return done;
 }
 
 __host__ __device__ __forceinline__ int up(int a, int b) { return (a + b - 1) / b * b; }
@@ -212,6 +214,24 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, uint32_t chunk, const CU
                                           int row, int b) {
 #pragma unroll
   for (int c = 0; c < HD / 64; ++c) tma_load_3d(dst + c * chunk, m, bar, col + c * 64, row, b);
+}
+
+// N consecutive TMEM columns of this thread's row
+template <int N>
+__device__ __forceinline__ void tmem_row(float (&x)[N], uint32_t addr) {
+  if constexpr (N % 32 == 0) {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tmem_ld32(addr + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
+  } else {
+    static_assert(N == 16, "HD / 4");
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+  }
+  tmem_ld_wait();
 }
 
 // w rows of a key tile (w a multiple of 16), in one box of KB rows where they are more than 32
@@ -405,30 +425,28 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     const float sl2 = p.scale * kLog2e;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    // the first NC columns of a block
-    const auto block = [&](auto nc, auto mask, int k0, int j) {
-      constexpr int NC = decltype(nc)::value;
-      constexpr bool masked = decltype(mask)::value;
+    for (int j = 0; j < kb.n && ok; ++j) {
+      if (!(ok = warp_wait(s_full + (j & 1), (j >> 1) & 1))) break;
+      tc_fence_after();
+      const int k0 = kb.k0(j);
       const uint32_t tX = tS + (j & 1) * kKB + lanes;
-      float x[NC];
-#pragma unroll
-      for (int c = 0; c < NC; c += 32) tmem_ld32(tX + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
-      tmem_ld_wait();
-      if (masked) {
+      float x[kKB];
+      tmem_row<kKB>(x, tX);
+      if (!all_visible(q0, kQB, k0, kKB, p.window, p.sinks)) {  // also what lies behind a narrower block
         const uint64_t vis = visible_keys(i, k0, p.window, p.sinks);
         const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < kKB; ++c)
           if (!(bits[c / 32] >> (c % 32) & 1)) x[c] = -INFINITY;
       }
       float pm[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int c = 4; c < NC - 4; c += 8) {
+      for (int c = 4; c < kKB - 4; c += 8) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) pm[e] = max3(pm[e], x[c + 2 * e], x[c + 2 * e + 1]);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pm[e] = fmaxf(pm[e], x[NC - 4 + e]);
+      for (int e = 0; e < 4; ++e) pm[e] = fmaxf(pm[e], x[kKB - 4 + e]);
       const float bm = fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]) * sl2;
       float corr = 1.f;
       if (bm > m + 8.f) {
@@ -437,7 +455,7 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         l *= corr;
       }
       if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-        if (!(ok = warp_wait(v_empty + ((j - 1) & 1), ((j - 1) >> 1) & 1))) return;  // P V of j - 1 has been added
+        if (!(ok = warp_wait(v_empty + ((j - 1) & 1), ((j - 1) >> 1) & 1))) break;  // P V of j - 1 has been added
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
@@ -451,32 +469,21 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       }
       const float mm = m > -INFINITY ? m : 0.f;  // a row that sees nothing so far
       uint64_t ps[2] = {0, 0};
-      uint32_t w[NC / 2];
+      uint32_t w[kKB / 2];
       const uint64_t sl = f2(sl2, sl2), mn = f2(-mm, -mm);
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) {
+      for (int c = 0; c < kKB / 2; ++c) {
         float a0, a1;
-        ex2_of<masked ? 0 : 1>(c, fma2(f2(x[2 * c], x[2 * c + 1]), sl, mn), a0, a1);
+        ex2_of<1>(c, fma2(f2(x[2 * c], x[2 * c + 1]), sl, mn), a0, a1);
         ps[c & 1] = add2(ps[c & 1], f2(a0, a1));
         w[c] = pack2(a0, a1);
       }
       float l0, l1;
       unpack(add2(ps[0], ps[1]), l0, l1);
       l += l0 + l1;
-#pragma unroll
-      for (int c = 0; c < NC / 2; c += 16) tmem_st16(tX + c, w + c);
+      tmem_st16(tX, w);
+      tmem_st16(tX + 16, w + 16);
       tmem_st_wait();
-    };
-    for (int j = 0; j < kb.n && ok; ++j) {
-      if (!(ok = warp_wait(s_full + (j & 1), (j >> 1) & 1))) break;
-      tc_fence_after();
-      const int k0 = kb.k0(j);
-      if (all_visible(q0, kQB, k0, kKB, p.window, p.sinks))
-        block(std::integral_constant<int, kKB>{}, std::false_type{}, k0, j);
-      else if (kb.width(j) <= 32)
-        block(std::integral_constant<int, 32>{}, std::true_type{}, k0, j);
-      else
-        block(std::integral_constant<int, kKB>{}, std::true_type{}, k0, j);
       tc_fence_before();
       mbar_arrive(p_full + (j & 1));
     }
@@ -559,24 +566,6 @@ __device__ __forceinline__ void stage_grad(uint8_t* tile, uint32_t chunk, int ro
     put(part * Q4 + e + HALF, hi + e);
   }
 }
-// N consecutive TMEM columns of this thread's row
-template <int N>
-__device__ __forceinline__ void tmem_row(float (&x)[N], uint32_t addr) {
-  if constexpr (N % 32 == 0) {
-#pragma unroll
-    for (int c = 0; c < N; c += 32) tmem_ld32(addr + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
-  } else {
-    static_assert(N == 16, "HD / 4");
-    uint32_t* r = reinterpret_cast<uint32_t*>(x);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
-  }
-  tmem_ld_wait();
-}
-
 // What the dK / dV kernel reads of a query: its lse in units of log2 (infinity behind the sequence, which
 // makes its P zero) and D. Two rows of S rounded up to 128 for each sequence and head, in front of the scratch.
 __host__ __device__ __forceinline__ int64_t stat_row(int b, int h, int hq, int S) {
@@ -792,52 +781,36 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       const float D = sD[r];
       const uint64_t ln = f2(-lse2, -lse2), Dn = f2(-D, -D);
       p.D[stat_row(tile.b, tile.h, p.hq, p.S) + g * up(p.S, kQB) + i] = g ? D : lse2;
-      // columns [64 g, 64 g + NC) of a block
-      const auto block = [&](auto nc, auto mask, int k0) {
-        constexpr int NC = decltype(nc)::value;
-        constexpr bool masked = decltype(mask)::value;
-        float a[NC], y[NC];
-        tmem_row<NC>(a, tX);
+      for (int j = 0; j < kb.n && ok; ++j, ++jj) {  // columns [64 g, 64 g + 64) of each block
+        if (!(ok = warp_wait(s_full, jj & 1))) break;
+        tc_fence_after();
+        const int k0 = kb.k0(j);
+        float a[64], y[64];
+        uint32_t w[32];
+        tmem_row<64>(a, tX);
         tc_fence_before();
         mbar_arrive(s_free);
 #pragma unroll
-        for (int c = 0; c < NC / 2; ++c)
-          ex2_of<masked ? 0 : 2>(c, fma2(f2(a[2 * c], a[2 * c + 1]), sl, ln), a[2 * c], a[2 * c + 1]);
-        if (masked) {
+        for (int c = 0; c < 32; ++c) ex2_of<2>(c, fma2(f2(a[2 * c], a[2 * c + 1]), sl, ln), a[2 * c], a[2 * c + 1]);
+        if (!all_visible(q0, kQB, k0, kKB, p.window, p.sinks)) {  // also what lies behind a narrower block
           const uint64_t vis = visible_keys(i, k0 + g * 64, p.window, p.sinks);
           const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
+          for (int c = 0; c < 64; ++c)
             if (!(bits[c / 32] >> (c % 32) & 1)) a[c] = 0.f;
         }
-        if (!(ok = warp_wait(dp_full, jj & 1))) return;
+        if (!(ok = warp_wait(dp_full, jj & 1))) break;
         tc_fence_after();
-        tmem_row<NC>(y, tY);
-        uint32_t w[NC / 2];
+        tmem_row<64>(y, tY);
 #pragma unroll
-        for (int c = 0; c < NC / 2; ++c) {
+        for (int c = 0; c < 32; ++c) {
           float d0, d1;
           unpack(mul2(f2(a[2 * c], a[2 * c + 1]), add2(f2(y[2 * c], y[2 * c + 1]), Dn)), d0, d1);
           w[c] = pack2(d0, d1);
         }
-#pragma unroll
-        for (int c = 0; c < NC / 2; c += 16) tmem_st16(tY + c, w + c);
+        tmem_st16(tY, w);
+        tmem_st16(tY + 16, w + 16);
         tmem_st_wait();
-      };
-      for (int j = 0; j < kb.n && ok; ++j, ++jj) {
-        if (!(ok = warp_wait(s_full, jj & 1))) break;
-        tc_fence_after();
-        const int k0 = kb.k0(j);
-        if (all_visible(q0, kQB, k0, kKB, p.window, p.sinks)) {
-          block(std::integral_constant<int, 64>{}, std::false_type{}, k0);
-        } else if (kb.width(j) > 32) {
-          block(std::integral_constant<int, 64>{}, std::true_type{}, k0);
-        } else if (g == 0) {
-          block(std::integral_constant<int, 32>{}, std::true_type{}, k0);
-        } else {
-          mbar_arrive(s_free);
-          ok = warp_wait(dp_full, jj & 1);
-        }
         tc_fence_before();
         mbar_arrive(ds_full);
       }
@@ -1037,22 +1010,15 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
       float x[64], y[64];
       uint32_t w[32];
       tmem_row<64>(x, tX);
-      if (all_visible(q, C::QB, k0, kQB, p.window, p.sinks)) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 l4 = lse[c / 4];
-          ex2_of<2>(c / 2, fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
-          ex2_of<2>(c / 2 + 1, fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
-        }
-      } else {
+      for (int c = 0; c < 64; c += 4) {
+        const float4 l4 = lse[c / 4];
+        ex2_of<2>(c / 2, fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
+        ex2_of<2>(c / 2 + 1, fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
+      }
+      if (!all_visible(q, C::QB, k0, kQB, p.window, p.sinks)) {
         const uint64_t vis = visible_queries(key, q + half * 64, p.window, p.sinks);
         const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
-#pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 l4 = lse[c / 4];
-          ex2_of<0>(c / 2, fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
-          ex2_of<0>(c / 2 + 1, fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
-        }
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           if (!(bits[c / 32] >> (c % 32) & 1)) x[c] = 0.f;
