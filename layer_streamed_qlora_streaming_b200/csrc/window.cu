@@ -60,8 +60,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // 2^x of a pair on the FMA pipe: x = n + f with n the nearest whole number (by adding 1.5 * 2^23, whose low
 // bits then hold n), 2^f on [-1/2, 1/2] by the polynomial of degree 4 of least relative error (2.7e-6, by
 // Remez' exchange), n added to its exponent. For x up to 120; 0 below -125 and for -infinity. The
-// exponential unit gives 16 values a clock and SM, so a tile of 128 x 128 takes it 1024 clocks, as long as
-// two of its matrix products: a share of the pairs goes this way.
+// exponential unit gives 16 values a clock and SM, 1024 clocks for a tile of 128 x 128, and in the backward
+// kernels the threads' chain is what a block takes: of the backward of 8192 tokens none of the pairs on the
+// FMA pipe take 532 us, a quarter 524, half 513, three quarters 531. (The forward, with two CTAs an SM,
+// is not bound by it: 289 us with none, 295 with a quarter.)
 __device__ __forceinline__ void ex2_pair(uint64_t x, float& r0, float& r1) {
   constexpr float kMagic = 12582912.f;
   const uint64_t t = add2(x, f2(kMagic, kMagic)), f = fma2(add2(t, f2(-kMagic, -kMagic)), f2(-1.f, -1.f), x);
@@ -76,10 +78,9 @@ __device__ __forceinline__ void ex2_pair(uint64_t x, float& r0, float& r1) {
   r0 = x0 < -125.f ? 0.f : __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
   r1 = x1 < -125.f ? 0.f : __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
 }
-// 2^x of pair n of a run; with POLY of every 4 pairs by ex2_pair
-template <int POLY>
+// 2^x of pair n of a run, every other one by ex2_pair
 __device__ __forceinline__ void ex2_of(int n, uint64_t x, float& r0, float& r1) {
-  if (n % 4 < POLY) {
+  if (n % 2 == 0) {
     ex2_pair(x, r0, r1);
   } else {
     unpack(x, r0, r1);
@@ -474,7 +475,9 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 #pragma unroll
       for (int c = 0; c < kKB / 2; ++c) {
         float a0, a1;
-        ex2_of<1>(c, fma2(f2(x[2 * c], x[2 * c + 1]), sl, mn), a0, a1);
+        unpack(fma2(f2(x[2 * c], x[2 * c + 1]), sl, mn), a0, a1);
+        a0 = ex2_approx(a0);
+        a1 = ex2_approx(a1);
         ps[c & 1] = add2(ps[c & 1], f2(a0, a1));
         w[c] = pack2(a0, a1);
       }
@@ -791,7 +794,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         tc_fence_before();
         mbar_arrive(s_free);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) ex2_of<2>(c, fma2(f2(a[2 * c], a[2 * c + 1]), sl, ln), a[2 * c], a[2 * c + 1]);
+        for (int c = 0; c < 32; ++c) ex2_of(c, fma2(f2(a[2 * c], a[2 * c + 1]), sl, ln), a[2 * c], a[2 * c + 1]);
         if (!all_visible(q0, kQB, k0, kKB, p.window, p.sinks)) {  // also what lies behind a narrower block
           const uint64_t vis = visible_keys(i, k0 + g * 64, p.window, p.sinks);
           const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
@@ -1013,8 +1016,8 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
       for (int c = 0; c < 64; c += 4) {
         const float4 l4 = lse[c / 4];
-        ex2_of<2>(c / 2, fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
-        ex2_of<2>(c / 2 + 1, fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
+        ex2_of(c / 2, fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
+        ex2_of(c / 2 + 1, fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
       }
       if (!all_visible(q, C::QB, k0, kQB, p.window, p.sinks)) {
         const uint64_t vis = visible_queries(key, q + half * 64, p.window, p.sinks);
@@ -1144,32 +1147,55 @@ __global__ void __launch_bounds__(256) k_window_join(const WinBwdArgs p, const S
   }
 }
 
-// How the dK / dV work is cut: the parts of a tile are chosen for the fewest rounds of a B200's SMs times
-// what a round takes, a CTA costing about 3 blocks besides its own (start, tiles of K and V, stores).
-Split plan_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
+// How the dK / dV work is cut, by the estimated time in blocks: a CTA costs about 3 besides its own (start,
+// tiles of K and V, stores), the joining kernel about 5, and the CTAs that do not all start at once end on
+// average half a CTA after the SMs' mean (the tiles with sinks, the longest, start first).
+Split make_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
   constexpr int sms = 148;
-  const int64_t B = T / S;
+  const int64_t units = T / S * hkv;
   const int grp = hq / hkv;
   Split s;
   s.nkb = (S + kQB - 1) / kQB;
   s.nsb = (int)(((int64_t)std::min(sinks, S) + kQB - 1) / kQB);
   s.nq = s.nkb;
   s.near = (int)std::min<int64_t>(s.nq, ((int64_t)kQB - 2 + std::min(window, S)) / kQB + 1);
-  const int64_t tw = (int64_t)grp * s.near, ts = (int64_t)grp * s.nq;
-  int64_t best = INT64_MAX;
-  s.ps = s.pw = 1;
-  for (int n = 1; n <= 16 && (n == 1 || tw / n >= 2); ++n) {
-    const int64_t len = (tw + n - 1) / n;
-    const int64_t ps = std::min<int64_t>((ts + len - 1) / len, 4096);
-    const int64_t ctas = B * hkv * (s.nsb * ps + (int64_t)(s.nkb - s.nsb) * n);
-    const int64_t cost = ((ctas + sms - 1) / sms) * (len + 3);
-    if (cost < best) {
-      best = cost;
+  const int64_t tw = (int64_t)grp * s.near, ts = (int64_t)grp * s.nq;  // of the longest tiles
+  int64_t work = 0;
+  for (int kb = 0; kb < s.nkb; ++kb) work += (int64_t)grp * s.blocks(kb);
+  double best = 0;
+  int bs = 0, bw = 0;
+  for (int pw = 1; pw <= 16 && (pw == 1 || tw / pw >= 2); ++pw) {
+    for (int64_t ps = 1; s.nsb > 0 ? ps <= 256 && (ps == 1 || ts / ps >= 2) : ps == 1; ps += ps < 16 ? 1 : ps / 8) {
       s.ps = (int)ps;
-      s.pw = n;
+      s.pw = pw;
+      const int64_t ctas = units * s.ctas();
+      const int64_t len = std::max(s.nsb < s.nkb ? (tw + pw - 1) / pw : 0, s.nsb > 0 ? (ts + ps - 1) / ps : 0) + 3;
+      double cost = ctas <= sms ? (double)len : std::max((double)len, (double)(units * work + 3 * ctas) / sms + 0.5 * len);
+      if (joined_parts(s) > 0) cost += 5;
+      if (bw == 0 || cost < best) {
+        best = cost;
+        bs = (int)ps;
+        bw = pw;
+      }
     }
   }
+  s.ps = bs;
+  s.pw = bw;
   return s;
+}
+// The same, kept for a thread's next call: a model's layers ask for the same sizes.
+Split plan_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
+  struct Key {
+    int64_t T;
+    int S, hq, hkv, window, sinks;
+  };
+  static thread_local Key last{0, 0, 0, 0, 0, 0};
+  static thread_local Split split;
+  if (last.T != T || last.S != S || last.hq != hq || last.hkv != hkv || last.window != window || last.sinks != sinks) {
+    split = make_split(T, S, hq, hkv, window, sinks);
+    last = Key{T, S, hq, hkv, window, sinks};
+  }
+  return split;
 }
 
 // 3D map of a [B, S, cols] bf16 tensor with row stride ld: boxes of `rows` rows x 64 columns, 128-byte swizzle,
