@@ -320,6 +320,29 @@ struct QueryTile {
   }
 };
 
+// The same for a CTA that takes every step-th tile, without a division a tile.
+struct TileWalk : QueryTile {
+  int nq, hq, dh, dq, db;
+  __device__ __forceinline__ TileWalk(int x, int step, int hq_, int S) : QueryTile(x, hq_, S) {
+    hq = hq_;
+    nq = (S + kQB - 1) / kQB;
+    dh = step % hq;
+    dq = step / hq % nq;
+    db = step / hq / nq;
+  }
+  __device__ __forceinline__ void next() {
+    h += dh;
+    const int carry = h >= hq;
+    if (carry) h -= hq;
+    q0 -= (dq + carry) * kQB;
+    b += db;
+    if (q0 < 0) {
+      q0 += nq * kQB;
+      ++b;
+    }
+  }
+};
+
 template <int HD>
 struct FwdCfg {
   static constexpr int KB = 64;  // keys of a block
@@ -508,11 +531,6 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 #pragma unroll
         for (int e = 0; e < 32; ++e) w[e] = pack2(y[2 * e], y[2 * e + 1]);
         stage_row(sQ + c / 64 * C::CH, r, w);
-        if (p.o32 && i < p.S) {
-          float* d32 = p.o32 + (t * p.hq + h) * HD + c;
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) *reinterpret_cast<float4*>(d32 + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-        }
       }
       fence_proxy_async();
     }
@@ -576,9 +594,9 @@ __host__ __device__ __forceinline__ int64_t stat_row(int b, int h, int hq, int S
 }
 
 // ---------------------------------------------------------------------------------- dQ
-// Persistent CTAs, one an SM, taking the query tiles in turn; 320 threads: warp 0 TMA (the next tile's Q and
-// dO, two K and two V blocks of 128 keys in flight), warp 1 the MMAs, warps 2-9 two threads a query row
-// (half of a block's columns each).
+// Persistent CTAs, one an SM, taking the query tiles in turn; 320 threads: warp 0 TMA, warp 1 the MMAs, warps 2-9 two threads a query row
+// (half of a block's columns each); the next tile's Q, dO and o, two K blocks and one V block of 128 keys
+// are in flight.
 // Q and dO are copied into TMEM first and serve as the A operands from there: read from shared memory for
 // every block they took its whole bandwidth (128 bytes a clock: with K, V, their loads and dS K 1800
 // clocks a block, where the tensor cores take 1540), and their place is free for the next tile's.
@@ -595,22 +613,25 @@ struct DqCfg {
   static constexpr uint32_t SMEM = 7 * TILE + 1024 + 256 + kQB * 4;
 };
 
-template <int HD, bool O32>
+template <int HD>
 __global__ void __launch_bounds__(320, 1)
 k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
             const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
             const __grid_constant__ CUtensorMap tmK16, const __grid_constant__ CUtensorMap tmV16,
-            const __grid_constant__ CUtensorMap tmDq, const WinBwdArgs p, const int tiles) {
+            const __grid_constant__ CUtensorMap tmDq, const __grid_constant__ CUtensorMap tmFo, const WinBwdArgs p,
+            const int tiles) {
   using C = DqCfg<HD>;
   constexpr int kKB = C::KB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sQ = smem, *sO = smem + C::TILE, *sK = smem + 2 * C::TILE, *sV = smem + 4 * C::TILE, *sG = smem + 6 * C::TILE;
+  uint8_t *sQ = smem, *sO = smem + C::TILE, *sF = smem + 2 * C::TILE, *sK = smem + 3 * C::TILE, *sV = smem + 5 * C::TILE,
+          *sG = smem + 6 * C::TILE;  // Q, dO, o, K [2], V, dQ on its way out
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 7 * C::TILE);
   uint64_t *a_full = bars, *s_free = bars + 1, *ds_full = bars + 2;  // of all 256 row threads
   uint64_t *q_full = bars + 3, *s_full = bars + 4, *dp_full = bars + 5, *done = bars + 6;
-  uint64_t *k_full = bars + 7, *k_empty = bars + 9, *v_full = bars + 11, *v_empty = bars + 13;  // [2]
-  constexpr int kBars = 15;
+  uint64_t *k_full = bars + 7, *k_empty = bars + 9;  // [2]
+  uint64_t *v_full = bars + 11, *v_empty = bars + 12;
+  constexpr int kBars = 13;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   float* sD = reinterpret_cast<float*>(bars + kBars + 1);  // [128]
   const int grp = p.hq / p.hkv;
@@ -626,6 +647,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmDq);
+    tma_prefetch_desc(&tmFo);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -643,26 +665,26 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   if (warp == 0) {
     bool ok = true;
     int it = 0, jj = 0;
-    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it) {
-      const QueryTile tile(x, p.hq, p.S);
+    TileWalk tile(blockIdx.x, gridDim.x, p.hq, p.S);
+    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it, tile.next()) {
       const Blocks<kKB> kb(tile.q0, p.S, p.window, p.sinks);
       const int kvh = tile.h / grp;
-      if (it > 0 && !(ok = warp_wait(a_full, (it - 1) & 1))) break;  // the last tile's Q and dO have been copied
+      if (it > 0 && !(ok = warp_wait(a_full, (it - 1) & 1))) break;  // the last tile's have been copied
       if (elect_one()) {
-        mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+        mbar_arrive_expect_tx(q_full, 3 * C::TILE);
         load_tile<HD>(sQ, C::CH, &tmQ, q_full, tile.h * HD, tile.q0, tile.b);
         load_tile<HD>(sO, C::CH, &tmO, q_full, tile.h * HD, tile.q0, tile.b);
+        load_tile<HD>(sF, C::CH, &tmFo, q_full, tile.h * HD, tile.q0, tile.b);
       }
       __syncwarp();
       for (int j = 0; j < kb.n && ok; ++j, ++jj) {
         const int k0 = kb.k0(j), w = kb.width(j), s = jj & 1;
-        for (int kv = 0; kv < 2; ++kv) {
-          if (jj >= 2 && !(ok = warp_wait((kv ? v_empty : k_empty) + s, ((jj >> 1) - 1) & 1))) break;
-          if (elect_one())
-            load_keys<HD, kKB>((kv ? sV : sK) + s * C::TILE, C::CH, kv ? &tmV : &tmK, kv ? &tmV16 : &tmK16,
-                               (kv ? v_full : k_full) + s, kvh * HD, k0, w, tile.b);
-          __syncwarp();
-        }
+        if (jj >= 2 && !(ok = warp_wait(k_empty + s, ((jj >> 1) - 1) & 1))) break;
+        if (elect_one()) load_keys<HD, kKB>(sK + s * C::TILE, C::CH, &tmK, &tmK16, k_full + s, kvh * HD, k0, w, tile.b);
+        __syncwarp();
+        if (jj >= 1 && !(ok = warp_wait(v_empty, (jj - 1) & 1))) break;
+        if (elect_one()) load_keys<HD, kKB>(sV, C::CH, &tmV, &tmV16, v_full, kvh * HD, k0, w, tile.b);
+        __syncwarp();
       }
     }
   } else if (warp == 1) {
@@ -678,18 +700,18 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       __syncwarp();
     };
     const auto dprobs = [&](int jj, int w) {  // dP = dO V^T
-      if (!(ok = ok && warp_wait(v_full + (jj & 1), (jj >> 1) & 1))) return;
+      if (!(ok = ok && warp_wait(v_full, jj & 1))) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_tt<HD>(tP, tA + 64, make_desc(smem_u32(sV + (jj & 1) * C::TILE), 16, 1024), C::CH, umma_idesc_bf16(128, w, 0, 0));
+        mma_tt<HD>(tP, tA + 64, make_desc(smem_u32(sV), 16, 1024), C::CH, umma_idesc_bf16(128, w, 0, 0));
         umma_commit(dp_full);
-        umma_commit(v_empty + (jj & 1));
+        umma_commit(v_empty);
       }
       __syncwarp();
     };
     int it = 0, jj = 0;
-    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it) {
-      const QueryTile tile(x, p.hq, p.S);
+    TileWalk tile(blockIdx.x, gridDim.x, p.hq, p.S);
+    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it, tile.next()) {
       const Blocks<kKB> kb(tile.q0, p.S, p.window, p.sinks);
       if (!(ok = warp_wait(a_full, it & 1))) break;
       scores(jj, kb.width(0));
@@ -720,53 +742,20 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     const float sl2 = p.scale * kLog2e;
     const uint64_t sl = f2(sl2, sl2);
     bool ok = true;
-    // D of a tile's rows, from the forward's unrounded o where it was kept: a warp takes 16 rows, HD / 8 lanes
-    // a row; o is fetched ahead
-    constexpr int LPR = HD / 8, RPI = 32 / LPR, ROWS = 16 / RPI;  // lanes a row, rows a load, loads
-    const int drow = (warp - 2) * 16 + lane / LPR, dcol = lane % LPR * 8;
-    uint4 ov[ROWS][O32 ? 2 : 1];
-    const auto fetch_o = [&](int x) {
-      if (x >= tiles) return;
-      const QueryTile t(x, p.hq, p.S);
-#pragma unroll
-      for (int n = 0; n < ROWS; ++n) {
-        const int row = t.q0 + drow + n * RPI;
-        const int64_t tt = (int64_t)t.b * p.S + row;
-#pragma unroll
-        for (int e = 0; e < (O32 ? 2 : 1); ++e) {
-          ov[n][e] = make_uint4(0, 0, 0, 0);
-          if (row < p.S)
-            ov[n][e] = O32 ? *reinterpret_cast<const uint4*>(p.o32 + (tt * p.hq + t.h) * HD + dcol + 4 * e)
-                           : *reinterpret_cast<const uint4*>(p.o + tt * p.ldo + (int64_t)t.h * HD + dcol);
-        }
-      }
+    TileWalk tile(blockIdx.x, gridDim.x, p.hq, p.S);
+    const auto load_lse = [&] {
+      return tile.q0 + r < p.S ? p.lse[((int64_t)tile.b * p.S + tile.q0 + r) * p.hq + tile.h] : INFINITY;
     };
-    fetch_o(blockIdx.x);
+    float lse = load_lse();  // fetched under the tile in front
     int it = 0, jj = 0;
     for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it) {
-      const QueryTile tile(x, p.hq, p.S);
-      const int q0 = tile.q0, i = q0 + r;
+      const int q0 = tile.q0, h = tile.h, b = tile.b, i = q0 + r;
       const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
-      const int64_t t = (int64_t)tile.b * p.S + i;
-      const float lse2 = i < p.S ? p.lse[t * p.hq + tile.h] * kLog2e : INFINITY;
       // a wait that runs out is shared at the next barrier, which every warp reaches
       ok = warp_wait(q_full, it & 1);
-#pragma unroll
-      for (int n = 0; n < ROWS; ++n) {
-        const int row = drow + n * RPI;
-        const uint4 dv = *reinterpret_cast<const uint4*>(sO + dcol / 64 * C::CH + row * 128 + ((dcol % 64 / 8) ^ (row & 7)) * 16);
-        const __nv_bfloat16* d8 = reinterpret_cast<const __nv_bfloat16*>(&dv);
-        const __nv_bfloat16* o8 = reinterpret_cast<const __nv_bfloat16*>(&ov[n][0]);
-        const float* f8 = reinterpret_cast<const float*>(&ov[n][0]);
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += __bfloat162float(d8[e]) * (O32 ? f8[e] : __bfloat162float(o8[e]));
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane % LPR == 0) sD[row] = sum;
-      }
-      {  // the first four warps copy Q's rows into TMEM, the others dO's
+      {  // the first four warps copy Q's rows into TMEM, the others dO's, forming D = dO . o as well
         const uint8_t* src = g ? sO : sQ;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c) {
           uint32_t w[32];
@@ -774,16 +763,34 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<uint4*>(w + 4 * e) = *reinterpret_cast<const uint4*>(src + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
           tmem_st32(tA + g * 64 + c * 32 + lanes, w);
+          if (g == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint4 o4 = *reinterpret_cast<const uint4*>(sF + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
+              const uint32_t o[4] = {o4.x, o4.y, o4.z, o4.w};
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float2 d2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(w + 4 * e + u));
+                const float2 o2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(o + u));
+                sum[u] = fmaf(d2.x, o2.x, fmaf(d2.y, o2.y, sum[u]));
+              }
+            }
+          }
         }
+        if (g == 1) sD[r] = i < p.S ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(a_full);
       }
       if (warp == 2) tma_store_wait();  // the last tile's dQ has left sG
       if (!(ok = sync_all(1, 256, ok))) break;
-      const float D = sD[r];
+      const float D = sD[r], lse2 = lse * kLog2e;
       const uint64_t ln = f2(-lse2, -lse2), Dn = f2(-D, -D);
-      p.D[stat_row(tile.b, tile.h, p.hq, p.S) + g * up(p.S, kQB) + i] = g ? D : lse2;
+      p.D[stat_row(b, h, p.hq, p.S) + g * up(p.S, kQB) + i] = g ? D : lse2;
+      if (x + gridDim.x < tiles) {
+        tile.next();
+        lse = load_lse();
+      }
       for (int j = 0; j < kb.n && ok; ++j, ++jj) {  // columns [64 g, 64 g + 64) of each block
         if (!(ok = warp_wait(s_full, jj & 1))) break;
         tc_fence_after();
@@ -817,7 +824,6 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         tc_fence_before();
         mbar_arrive(ds_full);
       }
-      fetch_o(x + gridDim.x);
       if ((ok = ok && warp_wait(done, it & 1))) {
         tc_fence_after();
         float lo[HD / 4], hi[HD / 4];
@@ -829,7 +835,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       if (!(ok = sync_all(1, 256, ok))) break;
       if (warp == 2 && elect_one()) {
 #pragma unroll
-        for (int c = 0; c < HD / 64; ++c) tma_store_3d(&tmDq, sG + c * C::CH, tile.h * HD + c * 64, q0, tile.b);
+        for (int c = 0; c < HD / 64; ++c) tma_store_3d(&tmDq, sG + c * C::CH, h * HD + c * 64, q0, b);
       }
       __syncwarp();
     }
@@ -1241,21 +1247,21 @@ cudaError_t launch_bwd(const WinBwdArgs& a, cudaStream_t s) {
   using Q = DqCfg<HD>;
   using K = DkvCfg<HD>;
   const int64_t B = a.T / a.S, cq = (int64_t)a.hq * HD, ck = (int64_t)a.hkv * HD;
-  CUtensorMap q, o, k, v, k16, v16, dq, dk, dv;
+  CUtensorMap q, o, k, v, k16, v16, dq, dk, dv, fo;
   if (!make_map3(&q, a.q, B, a.S, cq, a.ldq, kQB) || !make_map3(&o, a.dout, B, a.S, cq, a.lddo, kQB) ||
       !make_map3(&k, a.k, B, a.S, ck, a.ldk, Q::KB) || !make_map3(&v, a.v, B, a.S, ck, a.ldv, Q::KB) ||
       !make_map3(&k16, a.k, B, a.S, ck, a.ldk, 16) || !make_map3(&v16, a.v, B, a.S, ck, a.ldv, 16) ||
-      !make_map3(&dq, a.dq, B, a.S, cq, a.lddq, kQB) || !make_map3(&dk, a.dk, B, a.S, ck, a.lddk, kQB) ||
+      !make_map3(&dq, a.dq, B, a.S, cq, a.lddq, kQB) || !make_map3(&fo, a.o, B, a.S, cq, a.ldo, kQB) ||
+      !make_map3(&dk, a.dk, B, a.S, ck, a.lddk, kQB) ||
       !make_map3(&dv, a.dv, B, a.S, ck, a.lddv, kQB))
     return cudaErrorInvalidValue;
-  static std::atomic<unsigned long long> done_q{0}, done_q32{0}, done_k{0};
-  const auto dq_kernel = a.o32 ? k_window_dq<HD, true> : k_window_dq<HD, false>;
-  cudaError_t e = allow_smem(dq_kernel, Q::SMEM, a.o32 ? done_q32 : done_q);
+  static std::atomic<unsigned long long> done_q{0}, done_k{0};
+  cudaError_t e = allow_smem(k_window_dq<HD>, Q::SMEM, done_q);
   if (e == cudaSuccess) e = allow_smem(k_window_dkdv<HD>, K::SMEM, done_k);
   if (e != cudaSuccess) return e;
   const int tiles = (int)(B * a.hq * ((a.S + kQB - 1) / kQB));
-  e = launch_k(dq_kernel, dim3((unsigned)std::min(tiles, device_sm_count())), dim3(320), Q::SMEM, s, 0, q, o, k, v, k16,
-               v16, dq, a, tiles);
+  e = launch_k(k_window_dq<HD>, dim3((unsigned)std::min(tiles, device_sm_count())), dim3(320), Q::SMEM, s, 0, q, o, k, v, k16,
+               v16, dq, fo, a, tiles);
   note_launch(1);
   if (e != cudaSuccess) return e;
   const Split sp = plan_split(a.T, a.S, a.hq, a.hkv, a.window, a.sinks);
