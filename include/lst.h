@@ -199,6 +199,44 @@ lst_status lst_step_dpo(lst_ctx* ctx, const int32_t* tokens, const int32_t* targ
                         const int32_t* mask, int32_t n_pairs, int32_t seq, float beta, float* loss,
                         float* grads);
 
+/* How the terms of the policy loss are weighted (m_t = 1 on counted tokens, else 0): by
+ * m_t / sum m (mean over tokens), m_t / (nseq * sum of m over the token's sequence) (mean over the
+ * sequences of their means; a sequence without a counted token adds 0), m_t / T. */
+enum { LST_POLICY_TOKEN_MEAN = 0, LST_POLICY_SEQ_MEAN = 1, LST_POLICY_FIXED = 2 };
+
+typedef struct {
+  float clip_lo;        /* in [0, 1]: the ratio's lower bound is 1 - clip_lo */
+  float clip_hi;        /* >= 0: its upper bound is 1 + clip_hi; infinity: none */
+  float kl_beta;        /* >= 0, finite: weight of the KL term */
+  int32_t norm;         /* LST_POLICY_* */
+  int32_t adv_per_seq;  /* 1: one advantage a sequence [T / S]; 0: one a token [T] */
+} lst_policy;
+
+/* One policy-gradient step over the streamed base: the clipped surrogate with a KL term to the base with
+ * its adapters switched off (the reference model of lst_step_dpo), on n_seq sampled sequences of `seq`
+ * tokens (loss and weights as lst_k_policy_loss, lst_kernels.h). tokens, targets and mask are int32
+ * [n_seq * seq] (mask NULL: every position counts; it marks the sampled positions); old_logp [n_seq *
+ * seq]: the log-probabilities under which they were sampled, NULL: those of this step's own policy (its
+ * ratios are 1); adv: advantages [n_seq] or [n_seq * seq] (cfg->adv_per_seq). Targets of positions that
+ * do not count are not read for values. out: HOST float [4] = loss, mean KL estimate, share of clipped
+ * tokens, mean ratio, each weighted as cfg->norm says; grads as in lst_step. With kl_beta > 0 the step
+ * starts with the reference forward (3L layer reads instead of 2L, or fewer with reuse). The first call
+ * allocates the step's buffers (6 * max_batch * max_seq fp32 and a few). Needs vocab > 0,
+ * n_seq <= max_batch, seq <= max_seq. */
+lst_status lst_step_policy(lst_ctx* ctx, const int32_t* tokens, const int32_t* targets,
+                           const int32_t* mask, const float* old_logp, const float* adv, int32_t n_seq,
+                           int32_t seq, const lst_policy* cfg, float* out, float* grads);
+
+/* The per-token log-probabilities [n_seq * seq] of the last step's policy (before its optimizer
+ * update; 0 where the mask is 0) to dst (host or device): the old_logp of further updates on the same
+ * samples. LST_ERR_STATE unless the last step was lst_step_policy. */
+lst_status lst_get_logp(lst_ctx* ctx, float* dst);
+
+/* Attention of the next steps: query i sees key j <= i of its sequence when i - j < window or
+ * j < sinks. window 0 (default): plain causal attention. The backward's scratch is allocated by the
+ * first step that needs more of it. LST_ERR_ARG for negative values. */
+lst_status lst_set_attention_window(lst_ctx* ctx, int32_t window, int32_t sinks);
+
 /* Copy the last step's logits [batch * seq, V] fp32 to dst (host or device). */
 lst_status lst_get_logits(lst_ctx* ctx, float* dst);
 

@@ -155,19 +155,6 @@ lst_status lst_k_swiglu_bwd(const float* dm, const uint16_t* gu, int64_t T, int3
 lst_status lst_k_cross_entropy(const float* logits, int64_t T, int32_t V, const int32_t* targets,
                                float inv_T, float* loss_rows, uint16_t* dlogits, void* stream);
 
-/* How the terms of the policy loss are weighted (m_t = 1 on counted tokens, else 0): by
- * m_t / sum m (mean over tokens), m_t / (nseq * sum of m over the token's sequence) (mean over the
- * sequences of their means; a sequence without a counted token adds 0), m_t / T. */
-enum { LST_POLICY_TOKEN_MEAN = 0, LST_POLICY_SEQ_MEAN = 1, LST_POLICY_FIXED = 2 };
-
-typedef struct {
-  float clip_lo;        /* in [0, 1]: the ratio's lower bound is 1 - clip_lo */
-  float clip_hi;        /* >= 0: its upper bound is 1 + clip_hi; infinity: none */
-  float kl_beta;        /* >= 0, finite: weight of the KL term */
-  int32_t norm;         /* LST_POLICY_* */
-  int32_t adv_per_seq;  /* 1: one advantage a sequence [T / S]; 0: one a token [T] */
-} lst_policy;
-
 /* Clipped policy loss with a KL term and its gradient with respect to the logits, over T tokens in
  * sequences of S (T a multiple of S). Per counted token (mask[t] != 0; mask NULL: all):
  *   logp_t = logits[t][y_t] - logsumexp(logits[t]),  r = exp(logp_t - old_logp[t]),

@@ -44,6 +44,15 @@ class AdamW(C.Structure):
                 ("weight_decay", C.c_float), ("deferred", C.c_int32)]
 
 
+POLICY_TOKEN_MEAN, POLICY_SEQ_MEAN, POLICY_FIXED = 0, 1, 2
+
+
+class Policy(C.Structure):
+    """lst_policy: the clip range, the KL weight, the normalisation (POLICY_*), the advantages' layout."""
+    _fields_ = [("clip_lo", C.c_float), ("clip_hi", C.c_float), ("kl_beta", C.c_float), ("norm", C.c_int32),
+                ("adv_per_seq", C.c_int32)]
+
+
 class Stats(C.Structure):
     _fields_ = [("steps", C.c_int64), ("launches_last_step", C.c_int64),
                 ("layer_reads_last_step", C.c_int64), ("h2d_bytes_last_step", C.c_int64),
@@ -74,6 +83,9 @@ _SIGS = {
     "lst_set_profiling": (_I32, [_P, _I32]),
     "lst_apply_optimizer": (_I32, [_P, _P]),
     "lst_step_dpo": (_I32, [_P, _P, _P, _P, _I32, _I32, _F32, C.POINTER(C.c_float), _P]),
+    "lst_step_policy": (_I32, [_P, _P, _P, _P, _P, _P, _I32, _I32, _P, C.POINTER(C.c_float), _P]),
+    "lst_get_logp": (_I32, [_P, _P]),
+    "lst_set_attention_window": (_I32, [_P, _I32, _I32]),
     "lst_set_reuse": (_I32, [_P, _I32]),
     "lst_set_prefetch": (_I32, [_P, _I32]),
     "lst_plan_reads": (_I32, [_P, _I32, _I32, _I32, _P, _P, _P, _P]),
@@ -308,6 +320,24 @@ class Context:
                                   C.byref(loss), _ptr(grads)), self.h, "lst_step_dpo")
         return loss.value
 
+    def step_policy(self, tokens, targets, adv, n_seq: int, seq: int, old_logp=None, mask=None, clip_lo=0.2, clip_hi=0.2,
+                    kl_beta=0.0, norm=POLICY_SEQ_MEAN, adv_per_seq=True, grads=None) -> dict:
+        """Clipped policy-gradient step on n_seq sampled sequences (reference model: the base with the
+        adapters off); the loss, the mean KL estimate, the share of clipped tokens and the mean ratio."""
+        out = (C.c_float * 4)()
+        cfg = Policy(clip_lo, clip_hi, kl_beta, norm, int(bool(adv_per_seq)))
+        _check(lib().lst_step_policy(self.h, _ptr(tokens), _ptr(targets), _ptr(mask), _ptr(old_logp), _ptr(adv), n_seq,
+                                     seq, C.byref(cfg), out, _ptr(grads)), self.h, "lst_step_policy")
+        return {"loss": out[0], "kl": out[1], "clipped": out[2], "ratio": out[3]}
+
+    def logp(self, dst) -> None:
+        """Per-token log-probabilities of the last policy step (fp32 [n_seq * seq])."""
+        _check(lib().lst_get_logp(self.h, _ptr(dst)), self.h, "lst_get_logp")
+
+    def set_attention_window(self, window: int, sinks: int = 0) -> None:
+        """Attention of the next steps: a sliding window with sinks (window 0: plain causal)."""
+        _check(lib().lst_set_attention_window(self.h, int(window), int(sinks)), self.h, "lst_set_attention_window")
+
     def logits(self, dst) -> None:
         _check(lib().lst_get_logits(self.h, _ptr(dst)), self.h, "lst_get_logits")
 
@@ -482,15 +512,6 @@ def k_swiglu_bwd(dm, gu, T, F, dgu, stream=None):
 def k_cross_entropy(logits, T, V, targets, inv_T, loss_rows, dlogits, stream=None):
     _check(lib().lst_k_cross_entropy(_ptr(logits), T, V, _ptr(targets), inv_T, _ptr(loss_rows),
                                      _ptr(dlogits), _stream(stream)), what="lst_k_cross_entropy")
-
-
-POLICY_TOKEN_MEAN, POLICY_SEQ_MEAN, POLICY_FIXED = 0, 1, 2
-
-
-class Policy(C.Structure):
-    """lst_policy: the clip range, the KL weight, the normalisation (POLICY_*), the advantages' layout."""
-    _fields_ = [("clip_lo", C.c_float), ("clip_hi", C.c_float), ("kl_beta", C.c_float), ("norm", C.c_int32),
-                ("adv_per_seq", C.c_int32)]
 
 
 def policy_scratch(T, S) -> int:

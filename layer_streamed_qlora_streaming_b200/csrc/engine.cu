@@ -23,6 +23,8 @@
 #include "../../include/lst.h"
 #include "../../include/lst_kernels.h"
 #include "attention.cuh"
+#include "policy.cuh"
+#include "window.cuh"
 #include "common.cuh"
 #include "gemm.cuh"
 #include "lora.cuh"
@@ -260,7 +262,7 @@ struct NvtxRange {
   }
   ~NvtxRange() { nvtxRangePop(); }
 };
-enum HeadMode { HEAD_SFT = 0, HEAD_HIDDEN = 1, HEAD_DPO = 2 };
+enum HeadMode { HEAD_SFT = 0, HEAD_HIDDEN = 1, HEAD_DPO = 2, HEAD_POLICY = 3 };
 
 struct ReadPlan {
   int slot = 0;         // pool slot the read computes from
@@ -355,6 +357,16 @@ struct lst_ctx {
   int32_t* mask_dev = nullptr;  // [T] positions that count (DPO)
   bool have_mask = false;
   float dpo_beta = 0.f;
+  // policy step: allocated by the first one
+  lst_policy pol = {};
+  float *pol_old = nullptr, *pol_ref = nullptr, *pol_adv = nullptr, *pol_logp = nullptr;  // [T]
+  float *pol_out = nullptr, *pol_scratch = nullptr;                                       // [4], policy_scratch()
+  float* host_pol = nullptr;  // pinned [4]
+  bool have_old = false, have_logp = false;
+  // attention window (0: plain causal), its backward's scratch
+  int win = 0, sinks = 0;
+  float* win_scratch = nullptr;
+  int64_t win_floats = 0;
   bool logits_whole = false;  // the last step's logits are all in `logits`
   __nv_bfloat16* gbuf = nullptr;
   int32_t *tok = nullptr, *tgt = nullptr;
@@ -759,7 +771,15 @@ lst_status layer_fwd(lst_ctx* c, int i, const uint8_t* blob, const uint8_t* hdr,
     a.hd = c->hd;
     a.scale = 1.0f / std::sqrt((float)c->hd);
     ProfScope ps(c, c->stream, PC_ATTN);
-    CK(attention_fwd(a, c->stream));
+    if (c->win > 0) {
+      WinArgs w;
+      static_cast<AttnArgs&>(w) = a;
+      w.window = c->win;
+      w.sinks = c->sinks;
+      CK(window_fwd(w, c->stream));
+    } else {
+      CK(attention_fwd(a, c->stream));
+    }
   }
   TRY(wait_chunk(c, 1));
   TRY(group_fwd(c, i, G_O, blob, W, c->o, c->dq, c->h, c->d, 1, nullptr, x, true));
@@ -825,7 +845,16 @@ lst_status layer_bwd(lst_ctx* c, int i, const uint8_t* blob, const uint8_t* hdr,
     a.rope_cos = c->cos_t;  // dq and dk leave the kernel with the rotary embedding undone
     a.rope_sin = c->sin_t;
     ProfScope ps(c, c->stream, PC_ATTN);
-    CK(attention_bwd(a, c->stream));
+    if (c->win > 0) {
+      WinBwdArgs w;
+      static_cast<AttnBwdArgs&>(w) = a;
+      w.D = c->win_scratch;
+      w.window = c->win;
+      w.sinks = c->sinks;
+      CK(window_bwd(w, c->stream));
+    } else {
+      CK(attention_bwd(a, c->stream));
+    }
   }
   TRY(group_bwd(c, i, G_QKV, blob, W, c->dqkvb, c->dqkv, c->n1, c->d, c->dn, 1));
   TRY(flush_grads(c));  // before dout_b (the down group's dY) is overwritten below
@@ -974,8 +1003,82 @@ lst_status head_dpo(lst_ctx* c) {
   return LST_OK;
 }
 
-// An SFT step reads layers 0 .. L-1 (forward), then L-1 .. 0 (backward with recompute); a DPO step
-// first reads 0 .. L-1 once more for the reference forward (adapters off): 2L or 3L reads.
+PolicyArgs policy_args(const lst_ctx* c, bool reference) {
+  PolicyArgs a{};
+  a.logits = c->logits;
+  a.T = c->curT;
+  a.V = c->V;
+  a.S = (int)c->curS;
+  a.y = c->tgt;
+  a.mask = c->have_mask ? c->mask_dev : nullptr;
+  a.adv = c->pol_adv;
+  a.lo = c->pol.clip_lo;
+  a.hi = c->pol.clip_hi;
+  a.norm = c->pol.norm;
+  a.adv_per_seq = c->pol.adv_per_seq ? 1 : 0;
+  a.out = c->pol_out;
+  a.scratch = c->pol_scratch;
+  if (reference) {  // its log-probabilities only
+    a.logp = c->pol_ref;
+  } else {
+    a.old_logp = c->have_old ? c->pol_old : nullptr;
+    a.ref_logp = c->pol.kl_beta > 0.f ? c->pol_ref : nullptr;
+    a.beta = c->pol.kl_beta;
+    a.logp = c->pol_logp;
+    a.dlog = c->dlog;
+  }
+  return a;
+}
+
+// Head of the policy step: final norm, logits and the policy loss in passes of at most head_rows rows;
+// for the policy (not the reference pass) dlogits and the head's backward as well.
+lst_status head_policy(lst_ctx* c, bool reference) {
+  const int64_t T = c->curT;
+  const float* xL = c->xs + (int64_t)c->L * c->Tmax * c->d;
+  const PolicyArgs a = policy_args(c, reference);
+  {
+    ProfScope ps(c, c->stream, PC_OTHER);
+    CK(rmsnorm_fwd(xL, c->gf, T, c->d, c->cfg.rms_eps, c->nf, c->rstdf, c->stream));
+  }
+  const bool one_pass = T <= c->head_rows;
+  if (!one_pass) {
+    ProfScope ps(c, c->stream, PC_OTHER);
+    CK(policy_begin(a, c->stream));
+  }
+  for (int64_t r0 = 0; r0 < T; r0 += c->head_rows) {
+    const int64_t rows = std::min<int64_t>(c->head_rows, T - r0);
+    TRY(head_logits(c, r0, rows));
+    {
+      ProfScope ps(c, c->stream, PC_OTHER);
+      if (one_pass) CK(policy_begin(a, c->stream));
+      CK(policy_rows(a, r0, rows, one_pass, c->stream));
+    }
+    if (reference) continue;
+    GemmArgs g;
+    g.M = (int)rows;
+    g.N = c->d;
+    g.K = c->V;
+    g.A = c->dlog;
+    g.lda = c->V;
+    g.B = c->H;
+    g.ldb = c->d;
+    g.b_mn = 1;
+    g.C = c->dn + r0 * c->d;
+    g.ldc = c->d;
+    g.c_f32 = 1;
+    ProfScope ps(c, c->stream, PC_GEMM, 2.0 * rows * c->V * (double)c->d);
+    CK(gemm_bf16(g, c->stream));
+  }
+  if (reference) return LST_OK;
+  ProfScope ps(c, c->stream, PC_OTHER);
+  CK(cudaMemcpyAsync(c->loss_dev, c->pol_out, 4, cudaMemcpyDeviceToDevice, c->stream));
+  CK(cudaMemcpyAsync(c->host_pol, c->pol_out, 16, cudaMemcpyDeviceToHost, c->stream));
+  CK(rmsnorm_bwd(c->dn, xL, c->gf, c->rstdf, nullptr, T, c->d, c->ga, c->dout_b, c->stream));
+  return LST_OK;
+}
+
+// An SFT step reads layers 0 .. L-1 (forward), then L-1 .. 0 (backward with recompute); a DPO step, and
+// a policy step with a KL term, first reads 0 .. L-1 once more for the reference forward (adapters off): 2L or 3L reads.
 // plan_reads decides, for each read, the pool slot it computes from and whether the layer is
 // copied into that slot first:
 //  - reuse off: every read copies, into slot n % 2 (2L copies per step);
@@ -1184,7 +1287,7 @@ void build_reads(lst_ctx* c, HeadMode mode) {
   const int L = c->L;
   c->rd_layer.clear();
   c->rd_kind.clear();
-  if (mode == HEAD_DPO) {
+  if (mode == HEAD_DPO || (mode == HEAD_POLICY && c->pol.kl_beta > 0.f)) {
     for (int i = 0; i < L; ++i) {
       c->rd_layer.push_back(i);
       c->rd_kind.push_back(RD_REF);
@@ -1201,6 +1304,7 @@ void build_reads(lst_ctx* c, HeadMode mode) {
 }
 
 lst_status head_after(lst_ctx* c, int kind, HeadMode mode) {
+  if (mode == HEAD_POLICY) return head_policy(c, kind == RD_REF);
   if (kind == RD_REF) return head_ref(c);
   if (mode == HEAD_DPO) return head_dpo(c);
   if (mode == HEAD_SFT) return head_fwd_bwd(c);
@@ -1401,6 +1505,25 @@ lst_status finish_step(lst_ctx* c, float* loss, float* grads_out) {
 // destination gets one copy at the end of the step.
 void set_grads_dest(lst_ctx* c, float* grads) { c->grads_host = grads && is_pinned_host_ptr(grads) ? grads : nullptr; }
 
+// Scratch of the windowed attention backward for the step at hand, kept for the next ones.
+lst_status window_buffer(lst_ctx* c) {
+  if (c->win <= 0) return LST_OK;
+  if (!window_shape_ok(c->curT, (int)c->curS, c->hq, c->hkv, c->hd, c->win, c->sinks))
+    return fail(c, LST_ERR_ARG, "batch * seq too large for windowed attention");
+  const int64_t n = window_scratch(c->curT, (int)c->curS, c->hq, c->hkv, c->hd, c->win, c->sinks);
+  if (n <= c->win_floats) return LST_OK;
+  if (c->faults.fail_device()) return fail(c, LST_ERR_OOM, "device allocation failed (injected)");
+  CK(cudaStreamSynchronize(c->stream));  // a step that returned early may still use it
+  if (c->win_scratch) cudaFree(c->win_scratch);
+  c->dev_bytes -= c->win_floats * 4;
+  c->win_scratch = nullptr;
+  c->win_floats = 0;
+  CK(cudaMalloc(&c->win_scratch, (size_t)n * 4));
+  c->win_floats = n;
+  c->dev_bytes += n * 4;
+  return LST_OK;
+}
+
 lst_status begin_step(lst_ctx* c, int32_t batch, int32_t seq) {
   for (int i = 0; i < c->L; ++i)
     if (!c->registered[i]) return fail(c, LST_ERR_STATE, "layer " + std::to_string(i) + " is not registered");
@@ -1409,6 +1532,8 @@ lst_status begin_step(lst_ctx* c, int32_t batch, int32_t seq) {
   c->curB = batch;
   c->curS = seq;
   c->curT = (int64_t)batch * seq;
+  TRY(window_buffer(c));
+  c->have_logp = false;
   c->st.layer_reads_last_step = 0;
   c->st.h2d_bytes_last_step = 0;
   c->prof_used = 0;
@@ -1683,6 +1808,8 @@ void free_all(lst_ctx* c) {
   if (c->stage_gsum) cudaFree(c->stage_gsum);
   if (c->arena) cudaFreeHost(c->arena);
   if (c->host_loss) cudaFreeHost(c->host_loss);
+  if (c->host_pol) cudaFreeHost(c->host_pol);
+  if (c->win_scratch) cudaFree(c->win_scratch);
   for (auto e : c->ev_chunk) cudaEventDestroy(e);
   for (auto e : c->ev_free) cudaEventDestroy(e);
   for (auto e : c->ev_deqg) cudaEventDestroy(e);
@@ -1964,6 +2091,77 @@ lst_status lst_step_dpo(lst_ctx* c, const int32_t* tokens, const int32_t* target
   TRY(optimizer_update(c));
   c->have_logits = false;
   return finish_step(c, loss, grads);
+}
+
+// The buffers of the policy step, once.
+static lst_status policy_buffers(lst_ctx* c) {
+  if (!c->pol_old) TRY(dalloc(c, &c->pol_old, c->Tmax));
+  if (!c->pol_ref) TRY(dalloc(c, &c->pol_ref, c->Tmax));
+  if (!c->pol_adv) TRY(dalloc(c, &c->pol_adv, c->Tmax));
+  if (!c->pol_logp) TRY(dalloc(c, &c->pol_logp, c->Tmax));
+  if (!c->pol_out) TRY(dalloc(c, &c->pol_out, 4));
+  if (!c->pol_scratch) TRY(dalloc(c, &c->pol_scratch, policy_scratch(c->Tmax, 1)));
+  if (!c->host_pol && cudaMallocHost(&c->host_pol, 16) != cudaSuccess) {
+    cudaGetLastError();
+    c->host_pol = nullptr;
+    return fail(c, LST_ERR_OOM, "pinned host allocation failed");
+  }
+  return LST_OK;
+}
+
+lst_status lst_step_policy(lst_ctx* c, const int32_t* tokens, const int32_t* targets, const int32_t* mask,
+                           const float* old_logp, const float* adv, int32_t n_seq, int32_t seq, const lst_policy* cfg,
+                           float* out, float* grads) {
+  if (!c) return LST_ERR_ARG;
+  DeviceScope ds(c);
+  if (!tokens || !targets || !adv || !cfg || !out) return fail(c, LST_ERR_ARG, "null tokens/targets/adv/cfg/out");
+  if (c->V <= 0) return fail(c, LST_ERR_STATE, "lst_step_policy needs a head (vocab > 0)");
+  if (!policy_cfg_ok(cfg->clip_lo, cfg->clip_hi, cfg->kl_beta, cfg->norm)) return fail(c, LST_ERR_ARG, "bad policy loss parameters");
+  if (c->V > kPolicyMaxV) return fail(c, LST_ERR_ARG, "vocabulary too large for the policy loss");
+  TRY(policy_buffers(c));
+  TRY(begin_step(c, n_seq, seq));
+  TRY(copy_in(c, c->tok, tokens, c->curT * 4));
+  TRY(copy_in(c, c->tgt, targets, c->curT * 4));
+  c->pol = *cfg;
+  c->have_mask = mask != nullptr;
+  if (mask) TRY(copy_in(c, c->mask_dev, mask, c->curT * 4));
+  c->have_old = old_logp != nullptr;
+  if (old_logp) TRY(copy_in(c, c->pol_old, old_logp, c->curT * 4));
+  TRY(copy_in(c, c->pol_adv, adv, (cfg->adv_per_seq ? c->curB : c->curT) * 4));
+  {
+    ProfScope ps(c, c->stream, PC_OTHER);
+    CK(embed(c->tok, c->E, c->curT, c->d, c->V, c->xs, c->stream));
+  }
+  set_grads_dest(c, grads);
+  TRY(run_layers(c, HEAD_POLICY));
+  TRY(optimizer_update(c));
+  c->have_logits = false;
+  float loss = 0.f;
+  TRY(finish_step(c, &loss, grads));
+  for (int i = 0; i < 4; ++i) out[i] = c->host_pol[i];
+  c->have_logp = true;
+  return LST_OK;
+}
+
+lst_status lst_get_logp(lst_ctx* c, float* dst) {
+  if (!c) return LST_ERR_ARG;
+  DeviceScope ds(c);
+  if (!dst) return fail(c, LST_ERR_ARG, "null dst");
+  if (!c->have_logp) return fail(c, LST_ERR_STATE, "no log-probabilities: the last step was not lst_step_policy");
+  const bool dev = is_device_ptr(dst);
+  CK(cudaMemcpyAsync(dst, c->pol_logp, c->curT * 4, dev ? cudaMemcpyDeviceToDevice : cudaMemcpyDeviceToHost, c->stream));
+  CK(cudaStreamSynchronize(c->stream));
+  return LST_OK;
+}
+
+lst_status lst_set_attention_window(lst_ctx* c, int32_t window, int32_t sinks) {
+  if (!c) return LST_ERR_ARG;
+  if (window < 0 || sinks < 0) return fail(c, LST_ERR_ARG, "negative window or sinks");
+  if (window > 0 && !window_shape_ok(c->Tmax, c->cfg.max_seq, c->hq, c->hkv, c->hd, window, sinks))
+    return fail(c, LST_ERR_ARG, "max_batch * max_seq too large for windowed attention");
+  c->win = window;
+  c->sinks = window > 0 ? sinks : 0;
+  return LST_OK;
 }
 
 lst_status lst_get_logits(lst_ctx* c, float* dst) {

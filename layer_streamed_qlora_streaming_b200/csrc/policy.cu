@@ -540,10 +540,13 @@ cudaError_t launch_cluster(const PolicyArgs& a, int64_t row0, int64_t rows, int 
 
 int64_t policy_scratch(int64_t T, int S) { return 4 + 4 * T + T / S; }
 
+bool policy_cfg_ok(float lo, float hi, float beta, int norm) {
+  return lo >= 0.f && lo <= 1.f && hi >= 0.f && beta >= 0.f && beta < INFINITY && norm >= 0 && norm <= 2;
+}
+
 bool policy_args_ok(const PolicyArgs& a) {
-  return a.T > 0 && a.T <= INT32_MAX && a.V > 0 && a.V <= kPolicyMaxV && a.S > 0 && a.T % a.S == 0 && a.lo >= 0.f &&
-         a.lo <= 1.f && a.hi >= 0.f && a.beta >= 0.f && a.beta < INFINITY && (a.beta == 0.f || a.ref_logp) &&
-         a.norm >= 0 && a.norm <= 2;
+  return a.T > 0 && a.T <= INT32_MAX && a.V > 0 && a.V <= kPolicyMaxV && a.S > 0 && a.T % a.S == 0 &&
+         policy_cfg_ok(a.lo, a.hi, a.beta, a.norm) && (a.beta == 0.f || a.ref_logp);
 }
 
 cudaError_t policy_begin(const PolicyArgs& a, cudaStream_t s) {

@@ -30,6 +30,7 @@ struct PolicyArgs {
 
 int64_t policy_scratch(int64_t T, int S);
 constexpr int kPolicyMaxV = 1 << 20;
+bool policy_cfg_ok(float lo, float hi, float beta, int norm);
 bool policy_args_ok(const PolicyArgs& a);
 // The call is policy_begin, then policy_rows over ranges of rows that cover [0, T) once; the last row
 // to finish adds the row terms up in row order and writes out. The ranges may share one logits buffer.

@@ -175,3 +175,10 @@ def test_pointer_of_a_one_element_tensor_with_any_stride():
     assert lst._ptr(x.view(4, 2)[:, :1].t()[:, :1]) == x.data_ptr()
     with pytest.raises(ValueError):
         lst._ptr(x[::4])
+
+
+def test_null_context_is_refused():
+    L = lst.lib()
+    assert L.lst_set_attention_window(None, 4, 0) == 1
+    assert L.lst_get_logp(None, None) == 1
+    assert L.lst_step_policy(None, None, None, None, None, None, 1, 1, None, None, None) == 1
