@@ -23,14 +23,14 @@
 #include "../../include/lst.h"
 #include "../../include/lst_kernels.h"
 #include "attention.cuh"
-#include "policy.cuh"
-#include "window.cuh"
 #include "common.cuh"
 #include "gemm.cuh"
 #include "lora.cuh"
 #include "nf4.cuh"
 #include "ops.cuh"
 #include "optim.cuh"
+#include "policy.cuh"
+#include "window.cuh"
 
 #include <atomic>
 #include <cstdio>
@@ -1077,8 +1077,9 @@ lst_status head_policy(lst_ctx* c, bool reference) {
   return LST_OK;
 }
 
-// An SFT step reads layers 0 .. L-1 (forward), then L-1 .. 0 (backward with recompute); a DPO step, and
-// a policy step with a KL term, first reads 0 .. L-1 once more for the reference forward (adapters off): 2L or 3L reads.
+// An SFT step reads layers 0 .. L-1 (forward), then L-1 .. 0 (backward with recompute); a DPO step, and a
+// policy step with a KL term, first reads 0 .. L-1 once more for the reference forward (adapters off):
+// 2L or 3L reads.
 // plan_reads decides, for each read, the pool slot it computes from and whether the layer is
 // copied into that slot first:
 //  - reuse off: every read copies, into slot n % 2 (2L copies per step);
@@ -1506,11 +1507,11 @@ lst_status finish_step(lst_ctx* c, float* loss, float* grads_out) {
 void set_grads_dest(lst_ctx* c, float* grads) { c->grads_host = grads && is_pinned_host_ptr(grads) ? grads : nullptr; }
 
 // Scratch of the windowed attention backward for the step at hand, kept for the next ones.
-lst_status window_buffer(lst_ctx* c) {
+lst_status window_buffer(lst_ctx* c, int64_t T, int S) {
   if (c->win <= 0) return LST_OK;
-  if (!window_shape_ok(c->curT, (int)c->curS, c->hq, c->hkv, c->hd, c->win, c->sinks))
+  if (!window_shape_ok(T, S, c->hq, c->hkv, c->hd, c->win, c->sinks))
     return fail(c, LST_ERR_ARG, "batch * seq too large for windowed attention");
-  const int64_t n = window_scratch(c->curT, (int)c->curS, c->hq, c->hkv, c->hd, c->win, c->sinks);
+  const int64_t n = window_scratch(T, S, c->hq, c->hkv, c->hd, c->win, c->sinks);
   if (n <= c->win_floats) return LST_OK;
   if (c->faults.fail_device()) return fail(c, LST_ERR_OOM, "device allocation failed (injected)");
   CK(cudaStreamSynchronize(c->stream));  // a step that returned early may still use it
@@ -1529,10 +1530,10 @@ lst_status begin_step(lst_ctx* c, int32_t batch, int32_t seq) {
     if (!c->registered[i]) return fail(c, LST_ERR_STATE, "layer " + std::to_string(i) + " is not registered");
   if (batch <= 0 || seq <= 0 || batch > c->cfg.max_batch || seq > c->cfg.max_seq)
     return fail(c, LST_ERR_ARG, "batch/seq outside (0, max]");
+  TRY(window_buffer(c, (int64_t)batch * seq, seq));
   c->curB = batch;
   c->curS = seq;
   c->curT = (int64_t)batch * seq;
-  TRY(window_buffer(c));
   c->have_logp = false;
   c->st.layer_reads_last_step = 0;
   c->st.h2d_bytes_last_step = 0;

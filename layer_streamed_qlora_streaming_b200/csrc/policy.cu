@@ -73,50 +73,56 @@ __device__ __forceinline__ Token policy_token(const PolicyArgs& a, float A, floa
   return {make_float4(fmaf(a.beta, kl, -(cut ? cl : in)), kl, cut ? 1.f : 0.f, r), fmaf(a.beta, dkl, cut ? 0.f : -in)};
 }
 
-// One CTA: counts the mask and leaves the weight of a counted token of each sequence. A warp takes up to
-// 256 tokens of one sequence at a time, its loads independent; the counts are whole numbers, added in
-// shared memory in any order (in global memory, by one warp a sequence, where there are more sequences).
+// One CTA: counts the mask and leaves the weight of a counted token of each sequence. What is counted:
+// the whole mask (mean over tokens), each sequence's (mean over sequences), nothing (fixed). A warp takes up
+// to 256 tokens at a time, its loads independent; the counts are whole numbers, added in shared memory in
+// any order. More sequences than fit there are counted by a warp each, or by a thread each where they are
+// short (65536 sequences of one token: 2048 rounds of a load's latency by warps, 64 by threads).
 constexpr int kSeqs = 1024;
 __global__ void __launch_bounds__(1024) k_policy_weights(const int32_t* __restrict__ mask, int64_t T, int S, int norm,
                                                          float* __restrict__ scratch) {
   pdl_wait();
   pdl_trigger();
   __shared__ int count[kSeqs];
-  __shared__ unsigned long long total;
   float* w = seq_weight(scratch, T);
   const int nseq = (int)(T / S), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool few = nseq <= kSeqs;
-  if (threadIdx.x == 0) {
-    reinterpret_cast<unsigned*>(scratch)[0] = 0;
-    total = 0;
+  if (threadIdx.x == 0) reinterpret_cast<unsigned*>(scratch)[0] = 0;
+  if (norm == 1 && nseq > kSeqs) {
+    const bool wide = S >= 32;
+    for (int64_t u = wide ? warp : (int)threadIdx.x; u < nseq; u += wide ? 32 : 1024) {
+      int n = S;
+      if (mask) {
+        n = 0;
+        for (int i = wide ? lane : 0; i < S; i += wide ? 32 : 1) n += mask[u * S + i] != 0;
+        if (wide) n = __reduce_add_sync(0xffffffffu, n);
+      }
+      if (!wide || lane == 0) w[u] = n > 0 ? 1.f / ((float)nseq * (float)n) : 0.f;
+    }
+    return;
   }
-  if (few)
-    for (int b = threadIdx.x; b < nseq; b += 1024) count[b] = 0;
+  const int groups = norm == 0 ? 1 : norm == 1 ? nseq : 0, len = (int)(norm == 0 ? T : S);
+  for (int b = threadIdx.x; b < groups; b += 1024) count[b] = 0;
   __syncthreads();
-  const int step = few ? 256 : S, parts = (S + step - 1) / step;
-  for (int64_t u = warp; u < (int64_t)nseq * parts; u += 32) {
-    const int b = (int)(u / parts), i0 = (int)(u % parts) * step, i1 = min(S, i0 + step);
+  const int parts = (int)(((int64_t)len + 255) / 256);
+  for (int64_t u = warp; u < (int64_t)groups * parts; u += 32) {
+    const int b = (int)(u / parts);
+    const int64_t i0 = u % parts * 256, i1 = min((int64_t)len, i0 + 256);
     int n = 0;
     if (mask) {
-      const int32_t* m = mask + (int64_t)b * S;
-      for (int i = i0 + lane; i < i1; i += 256) {
+      const int32_t* m = mask + (int64_t)b * len + i0;
+      const int left = (int)(i1 - i0) - lane;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n += i + 32 * e < i1 && m[i + 32 * e] != 0;
-      }
+      for (int e = 0; e < 8; ++e) n += 32 * e < left && m[lane + 32 * e] != 0;
       n = __reduce_add_sync(0xffffffffu, n);
     } else {
-      n = i1 - i0;
+      n = (int)(i1 - i0);
     }
-    if (lane == 0) {
-      atomicAdd(&total, (unsigned long long)n);
-      if (few) atomicAdd(&count[b], n);
-      else w[b] = (float)n;
-    }
+    if (lane == 0) atomicAdd(&count[b], n);
   }
   __syncthreads();
   for (int b = threadIdx.x; b < nseq; b += 1024) {
-    const float n = few ? (float)count[b] : w[b];
-    w[b] = norm == 0 ? (total ? 1.f / (float)total : 0.f) : norm == 1 ? (n > 0.f ? 1.f / ((float)nseq * n) : 0.f) : 1.f / (float)T;
+    const float n = norm == 2 ? (float)T : norm == 0 ? (float)count[0] : (float)nseq * (float)count[b];
+    w[b] = n > 0.f ? 1.f / n : 0.f;
   }
 }
 
@@ -309,6 +315,7 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int 
       }
     }
     bulk_store_wait();
+    __syncwarp();  // with the row terms of the other lanes, too, in front of the arrival
     if (ok && claim()) {  // (the zeros are the consumers' from here on)
       if (lane == 0) {
         info[it & 3].lrow = -1;
@@ -558,8 +565,9 @@ cudaError_t policy_begin(const PolicyArgs& a, cudaStream_t s) {
 
 cudaError_t policy_rows(const PolicyArgs& a, int64_t row0, int64_t rows, bool early, cudaStream_t s) {
   if (!policy_args_ok(a) || row0 < 0 || rows <= 0 || row0 + rows > a.T) return cudaErrorInvalidValue;
-  // A CTA takes up to 4750 slots (224 consumers of 22, three half slices of shared memory), two CTAs an SM. A few rows are spread further, so
-  // that every SM has some of them, and a shorter slice is a shorter chain for a row.
+  // A CTA takes up to 4750 slots (224 consumers of 22, three half slices of shared memory), two CTAs an SM.
+  // A few rows are spread further, so that every SM has some of them, and a shorter slice is a shorter
+  // chain for a row.
   const int slots = (a.V + 6) / 4;
   int cs = 1;
   while (cs < 8 && ((slots + cs - 1) / cs > 4750 || (rows * cs < 2 * device_sm_count() && slots / cs > 1024))) cs *= 2;

@@ -302,13 +302,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc bb, uint32_t
 }
 
 // ---------------------------------------------------------------------------------- forward
-// One CTA per query tile of one head, two CTAs an SM, so that a CTA's start and end hide behind the
-// other's blocks. 192 threads: warp 0 TMA (two K and two V blocks of 64 keys in flight), warp 1 issues
-// the MMAs, warps 2-5 one thread a query row.
-//   S = Q K^T into one of two TMEM buffers; P = 2^(S' - m) as bf16 over S itself, the A operand of O += P V.
-// While a row's thread works on block j, the tensor cores form P V of j - 1 and S of j + 1.
-// The reference m of a row moves only when a block's maximum exceeds it by 2^8; O is then rescaled in
-// TMEM, once P V of j - 1 has been added. The tile of O leaves through Q's shared memory by TMA.
 // The query tile of CTA x: heads of a tile next to each other, the last tiles (the longest) first.
 struct QueryTile {
   int h, b, q0;
@@ -343,6 +336,13 @@ struct TileWalk : QueryTile {
   }
 };
 
+// One CTA per query tile of one head, two CTAs an SM, so that a CTA's start and end hide behind the
+// other's blocks. 192 threads: warp 0 TMA (two K and two V blocks of 64 keys in flight), warp 1 issues
+// the MMAs, warps 2-5 one thread a query row.
+//   S = Q K^T into one of two TMEM buffers; P = 2^(S' - m) as bf16 over S itself, the A operand of O += P V.
+// While a row's thread works on block j, the tensor cores form P V of j - 1 and S of j + 1.
+// The reference m of a row moves only when a block's maximum exceeds it by 2^8; O is then rescaled in
+// TMEM, once P V of j - 1 has been added. The tile of O leaves through Q's shared memory by TMA.
 template <int HD>
 struct FwdCfg {
   static constexpr int KB = 64;  // keys of a block
@@ -1281,7 +1281,7 @@ cudaError_t launch_bwd(const WinBwdArgs& a, cudaStream_t s) {
 
 bool window_shape_ok(int64_t T, int S, int hq, int hkv, int hd, int window, int sinks) {
   return (hd == 64 || hd == 128) && hq > 0 && hkv > 0 && hq % hkv == 0 && S > 0 && T > 0 && T % S == 0 &&
-         T <= INT32_MAX && T * hq <= INT32_MAX && T / S * hkv <= 65535 && window >= 1 && sinks >= 0;
+         S <= (1 << 30) && T <= INT32_MAX && T * hq <= INT32_MAX && T / S * hkv <= 65535 && window >= 1 && sinks >= 0;
 }
 
 int64_t window_scratch(int64_t T, int S, int hq, int hkv, int hd, int window, int sinks) {

@@ -103,6 +103,10 @@ class Case:
 @pytest.mark.parametrize("norm", list(NORMS))
 @pytest.mark.parametrize("nseq,S,V,per_seq,beta,offset", [
     (1, 1, 1, True, 0.1, 0),          # one token, one word
+    (1500, 1, 33, True, 0.1, 0),      # more sequences than are counted at once: of one token,
+    (1030, 33, 12, True, 0.1, 0),     # of more than a warp's width
+    (1025, 5, 40, False, 0.1, 0),     # and of fewer
+    (2, 1500, 20, True, 0.1, 0),      # sequences of several hundred tokens, over a short vocabulary
     (2, 3, 2, False, 0.1, 1),
     (4, 32, 512, True, 0.1, 0),
     (3, 17, 1001, False, 0.0, 3),     # odd vocabulary, odd base
