@@ -851,73 +851,129 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
 }
 
 // ---------------------------------------------------------------------------------- dK, dV
-// The work of one key tile of a kv head: its group's heads times the 128-row query blocks that see any
-// of its keys. It is cut into parts of equal length (n for the tiles that hold sinks, whose queries
-// reach to the end of the sequence, n for the others); with one part a CTA stores dK and dV itself,
-// else its fp32 sums go to the scratch and k_window_join adds them in order.
+// An item is 128 keys of a kv head against 128 queries of one of its heads. The items lie in a row: by sequence and
+// kv head (a unit), by key tile, by head, by query block. Each of the CTAs takes an equal share of the row, its cuts
+// in fixed places; what a tile costs besides its items (K, V, the stores) counts as kSeg items in front of
+// it, which also moves cuts next to a tile's border onto the border. The sums of a tile in one share are stored as dK and dV;
+// those of a cut tile go to the scratch as fp32, where k_window_join adds them in order. With few tiles
+// each is a CTA of its own (whole).
 struct Split {
-  int nkb, nsb;    // key tiles, those that hold sinks
-  int near;        // query blocks that see a tile through the window
-  int nq;          // query blocks of a sequence
-  int ps, pw;      // parts of a tile with sinks, of another
-  __host__ __device__ int ctas() const { return nsb * ps + (nkb - nsb) * pw; }  // a sequence and kv head
+  int nkb, nsb;   // key tiles of a sequence, those that hold sinks
+  int near;       // query blocks that see a tile through the window
+  int grp;        // heads of a kv head
+  int ctas, whole;
+  int64_t unit, total;  // length of a unit, of the row
+  // query blocks that see a key tile; all of the items in front of it in its unit
   __host__ __device__ int blocks(int kb) const {
-    const int n = nq - kb;
+    const int n = nkb - kb;
     return kb < nsb || n < near ? n : near;
   }
+  __host__ __device__ int64_t before(int kb) const;
+  __host__ __device__ int64_t start(int c) const {
+    return whole ? c / nkb * unit + before(c % nkb) : total * c / ctas;
+  }
 };
-// parts whose sums go to the scratch come first in its order, those of the tiles with sinks in front
-__host__ __device__ __forceinline__ int64_t joined_parts(const Split& s) {
-  return (s.ps > 1 ? (int64_t)s.nsb * s.ps : 0) + (s.pw > 1 ? (int64_t)(s.nkb - s.nsb) * s.pw : 0);
+constexpr int kSeg = 2;
+__host__ __device__ inline int64_t Split::before(int kb) const {
+  const auto falling = [&](int64_t k0, int64_t k1) { return k1 > k0 ? (k1 - k0) * (2 * (int64_t)nkb - k0 - k1 + 1) / 2 : 0; };
+  const int knee = nkb - near > nsb ? nkb - near : nsb;  // tiles from here on are seen to the sequence's end
+  int64_t n = falling(0, kb < nsb ? kb : nsb);
+  if (kb > nsb) n += (int64_t)near * ((kb < knee ? kb : knee) - nsb) + falling(knee, kb);
+  return n * grp + (int64_t)kSeg * kb;
+}
+// The tile that place v of the row lies in.
+struct TilePos {
+  int bk, kb;
+  int64_t first;  // place of its first item
+  __device__ __forceinline__ TilePos(const Split& sp, int64_t v) {
+    bk = (int)(v / sp.unit);
+    const int64_t r = v - bk * sp.unit;
+    int lo = 0, hi = sp.nkb - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (sp.before(mid) <= r) lo = mid;
+      else hi = mid - 1;
+    }
+    kb = lo;
+    first = bk * sp.unit + sp.before(kb) + kSeg;
+  }
+};
+// A CTA's share, tile by tile: items [i0, i1) of key tile kb of unit bk, seen by nqb query blocks. What it keeps
+// between tiles is little, 32 bits each: the kernel's threads have no registers to spare.
+struct Share {
+  int first, end;  // the next tile's first item, the share's end, counted from the share's start
+  int bk, kb;      // this tile's (before the first: in front of its tile)
+  int nqb, i0, i1;
+  __device__ __forceinline__ Share(const Split& sp, int c) {
+    const int64_t v = sp.start(c);
+    const TilePos at(sp, v);
+    first = (int)(at.first - v);
+    end = (int)(sp.start(c + 1) - v);
+    bk = at.bk;
+    kb = at.kb - 1;
+  }
+  __device__ __forceinline__ bool next(const Split& sp) {
+    while (first < end) {
+      if (++kb == sp.nkb) {
+        kb = 0;
+        ++bk;
+      }
+      nqb = sp.blocks(kb);
+      const int len = sp.grp * nqb;
+      i0 = max(-first, 0);
+      i1 = min(end - first, len);
+      first += len + kSeg;
+      if (i1 > i0) return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool all(const Split& sp) const { return i1 - i0 == sp.grp * nqb; }
+};
+
+// Where columns [col, col + 4) of dK (dv 0) or dV (dv 1) of CTA c's part lie in the scratch, in units of 4
+// floats: those of a tile's 128 rows one behind the other, as the threads that own a row each store them.
+// A CTA has at most two parts: the end of a tile (slot 0) and the start of another (slot 1).
+template <int HD>
+__device__ __forceinline__ int64_t part_at(int c, int slot, int dv, int col) {
+  return (((int64_t)c * 2 + slot) * 2 + dv) * (HD / 4 * kQB) + col / 4 * kQB;
 }
 
 template <int HD>
 struct DkvCfg {
-  static constexpr int QB = 128, NS = 2;                    // rows of a query block, blocks in flight
-  static constexpr uint32_t CH = kQB * 128;                // [128 x 64] bf16
+  static constexpr int QB = 128, NQ = 3, NO = 2;  // rows of a query block, blocks of Q and of dO in flight
+  static constexpr uint32_t CH = kQB * 128;      // [128 x 64] bf16
   static constexpr uint32_t TILE = (HD / 64) * CH;
-  static constexpr uint32_t STAGE = 2 * TILE + 2 * QB * 4;  // Q, dO, lse, D
-  static constexpr uint32_t SMEM = 2 * TILE + NS * STAGE + 1024 + 256;
+  static constexpr uint32_t SMEM = (2 + NQ + NO) * TILE + (NQ + NO) * QB * 4 + 256;
 };
 
 // 320 threads: warp 0 TMA, warp 1 the MMAs, warps 2-9 two threads a key row (half a block's queries each).
-//   S^T = K Q^T, P^T = 2^(S' - lse') as bf16 over it, the A operand of dV += P^T dO;
-//   dP^T = V dO^T, dS^T = P^T (dP^T - D) as bf16 over it, the A operand of dK += dS^T Q
-// (Q and dO read MN-major from the tiles used K-major for the scores). With dV, dK and both scores TMEM
-// is full. The threads turn S and dP in two steps, so that the tensor cores form dV of j and S of j + 1
-// under the second, dK of j and dP of j + 1 under the first step of j + 1. (Blocks of 64 queries with two
-// buffers of each took 2000 clocks a block and thus 4000 for these 128 queries: at N = 64 an MMA
-// is bound by shared memory, 48 clocks for 32, and by its issue.)
+//   S^T = K Q^T, P^T = 2^(S' - lse'), dP^T = V dO^T, dS^T = P^T (dP^T - D),
+//   dV += P^T dO, dK += dS^T Q with P^T and dS^T, as bf16 side by side over dP^T in TMEM, as A operands
+// (Q and dO read MN-major from the tiles used K-major for the scores). With dV, dK and both scores TMEM is
+// full; with K, V, three blocks of Q and two of dO shared memory is, too. P waits in registers for dP, so
+// that S of j + 1 is issued once the threads have read S of j, and dV and dK of j and dP of j + 1 run under the
+// exponentials of j + 1.
 template <int HD>
 __global__ void __launch_bounds__(320, 1)
 k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
               const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ CUtensorMap tmDk, const __grid_constant__ CUtensorMap tmDv, const WinBwdArgs p,
-              const Split sp, float* __restrict__ parts) {
+              const __grid_constant__ Split sp, float* __restrict__ parts) {
   using C = DkvCfg<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sK = smem, *sV = smem + C::TILE, *sQ = smem + 2 * C::TILE;  // [NS] stages
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sQ + C::NS * C::STAGE);
-  uint64_t *p_full = bars, *ds_full = bars + 1;  // of all 256 row threads
-  uint64_t *kv_full = bars + 2, *done = bars + 3, *s_full = bars + 4, *dp_full = bars + 5, *q_full = bars + 6,
-           *q_empty = bars + 6 + C::NS;
-  constexpr int kBars = 6 + 2 * C::NS;
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];  // no room to round up: its start is aligned
+  if (smem_u32(smem_tiles) & 1023) {  // for every thread alike
+    dev_fail(DEV_ERR_BAD_INDEX);
+    return;
+  }
+  uint8_t *sK = smem_tiles, *sV = sK + C::TILE, *sQ = sV + C::TILE, *sO = sQ + C::NQ * C::TILE;  // sQ [NQ], sO [NO]
+  float *sL = reinterpret_cast<float*>(sO + C::NO * C::TILE), *sD = sL + C::NQ * C::QB;          // lse [NQ], D [NO]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sD + C::NO * C::QB);
+  uint64_t *ds_full = bars, *s_free = bars + 1;  // of all 256 row threads
+  uint64_t *kv_full = bars + 2, *kv_free = bars + 3, *done = bars + 4, *s_full = bars + 5, *dp_full = bars + 6,
+           *q_full = bars + 7, *q_empty = q_full + C::NQ, *o_full = q_empty + C::NQ, *o_empty = o_full + C::NO;
+  constexpr int kBars = 7 + 2 * C::NQ + 2 * C::NO;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
-
-  const int grp = p.hq / p.hkv;
-  const int x = (int)blockIdx.x % sp.ctas(), bk = (int)blockIdx.x / sp.ctas();
-  const int b = bk / p.hkv, kvh = bk % p.hkv;
-  const bool sink = x < sp.nsb * sp.ps;
-  const int np = sink ? sp.ps : sp.pw, y = sink ? x : x - sp.nsb * sp.ps;
-  const int kb = sink ? y / np : sp.nsb + y / np, part = y % np;
-  const int k0 = kb * kQB, nqb = sp.blocks(kb);
-  const int64_t total = (int64_t)grp * nqb;
-  const int it0 = (int)(total * part / np), n = (int)(total * (part + 1) / np) - it0;
   const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  // item j of this CTA: its head and first query
-  const auto head = [&](int j) { return kvh * grp + (it0 + j) / nqb; };
-  const auto query = [&](int j) { return k0 + (it0 + j) % nqb * C::QB; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) mbar_init(bars + i, i < 2 ? 256 : 1);
@@ -939,161 +995,196 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot), tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
+  Share my(sp, blockIdx.x);
   pdl_wait();
   pdl_trigger();
 
-  if (n <= 0) {
-    // nothing of the work fell to this part
-  } else if (warp == 0) {
-    if (elect_one()) {
-      mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
-      load_tile<HD>(sK, C::CH, &tmK, kv_full, kvh * HD, k0, b);
-      load_tile<HD>(sV, C::CH, &tmV, kv_full, kvh * HD, k0, b);
-    }
-    __syncwarp();
-    for (int j = 0; j < n; ++j) {
-      const int s = j % C::NS, h = head(j), q = query(j);
-      if (j >= C::NS && !warp_wait(&q_empty[s], (j / C::NS - 1) & 1)) break;
-      if (elect_one()) {
-        uint8_t* st = sQ + s * C::STAGE;
+  // seg counts the CTA's tiles, jj its items: barrier phases run on over the tiles
+  int jj = 0;
+  bool ok = true;
+  if (warp == 0) {
+    for (int seg = 0; ok && my.next(sp); ++seg) {
+      const int b = my.bk / p.hkv, kvh = my.bk % p.hkv, k0 = my.kb * kQB;
+      int h = kvh * sp.grp + my.i0 / my.nqb, qb = my.i0 % my.nqb;
+      for (int j = my.i0; j < my.i1; ++j, ++jj) {
+        const int s = jj % C::NQ, t = jj % C::NO, q = k0 + qb * C::QB;
         const float* stat = p.D + stat_row(b, h, p.hq, p.S) + q;
-        mbar_arrive_expect_tx(&q_full[s], C::STAGE);
-        load_tile<HD>(st, C::CH, &tmQ, &q_full[s], h * HD, q, b);
-        bulk_load(st + 2 * C::TILE, stat, C::QB * 4, &q_full[s]);
-        bulk_load(st + 2 * C::TILE + C::QB * 4, stat + up(p.S, kQB), C::QB * 4, &q_full[s]);
-        load_tile<HD>(st + C::TILE, C::CH, &tmO, &q_full[s], h * HD, q, b);
+        if (jj >= C::NQ && !(ok = warp_wait(&q_empty[s], (jj / C::NQ - 1) & 1))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&q_full[s], C::TILE + C::QB * 4);
+          load_tile<HD>(sQ + s * C::TILE, C::CH, &tmQ, &q_full[s], h * HD, q, b);
+          bulk_load(sL + s * C::QB, stat, C::QB * 4, &q_full[s]);
+        }
+        __syncwarp();
+        if (j == my.i0) {
+          if (seg > 0 && !(ok = warp_wait(kv_free, (seg - 1) & 1))) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+            load_tile<HD>(sK, C::CH, &tmK, kv_full, kvh * HD, k0, b);
+            load_tile<HD>(sV, C::CH, &tmV, kv_full, kvh * HD, k0, b);
+          }
+          __syncwarp();
+        }
+        if (jj >= C::NO && !(ok = warp_wait(&o_empty[t], (jj / C::NO - 1) & 1))) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&o_full[t], C::TILE + C::QB * 4);
+          load_tile<HD>(sO + t * C::TILE, C::CH, &tmO, &o_full[t], h * HD, q, b);
+          bulk_load(sD + t * C::QB, stat + up(p.S, kQB), C::QB * 4, &o_full[t]);
+        }
+        __syncwarp();
+        if (++qb == my.nqb) {
+          qb = 0;
+          ++h;
+        }
       }
-      __syncwarp();
     }
   } else if (warp == 1) {
     constexpr uint32_t idS = umma_idesc_bf16(128, C::QB, 0, 0), idG = umma_idesc_bf16(128, HD, 0, 1);
-    bool ok = warp_wait(kv_full, 0);
-    const auto stage = [&](int j) { return smem_u32(sQ + j % C::NS * C::STAGE); };
+    const auto q_at = [&](int j) { return smem_u32(sQ + j % C::NQ * C::TILE); };
+    const auto o_at = [&](int j) { return smem_u32(sO + j % C::NO * C::TILE); };
     const auto scores = [&](int j) {  // S^T_j = K Q_j^T
-      if (!(ok = ok && warp_wait(&q_full[j % C::NS], (j / C::NS) & 1))) return;
+      if (!(ok = ok && warp_wait(&q_full[j % C::NQ], (j / C::NQ) & 1))) return;
       tc_fence_after();
       if (elect_one()) {
-        mma_ss<HD>(tS, make_desc(smem_u32(sK), 16, 1024), C::CH, make_desc(stage(j), 16, 1024), C::CH, idS);
+        mma_ss<HD>(tS, make_desc(smem_u32(sK), 16, 1024), C::CH, make_desc(q_at(j), 16, 1024), C::CH, idS);
         umma_commit(s_full);
       }
       __syncwarp();
     };
     const auto dprobs = [&](int j) {  // dP^T_j = V dO_j^T
+      if (!(ok = ok && warp_wait(&o_full[j % C::NO], (j / C::NO) & 1))) return;
+      tc_fence_after();
       if (elect_one()) {
-        mma_ss<HD>(tP, make_desc(smem_u32(sV), 16, 1024), C::CH, make_desc(stage(j) + C::TILE, 16, 1024), C::CH, idS);
+        mma_ss<HD>(tP, make_desc(smem_u32(sV), 16, 1024), C::CH, make_desc(o_at(j), 16, 1024), C::CH, idS);
         umma_commit(dp_full);
       }
       __syncwarp();
     };
-    scores(0);
-    if (ok) dprobs(0);
-    for (int j = 0; j < n && ok; ++j) {  // each half of a block's columns holds its own 64 queries' P and dS
-      if (!(ok = warp_wait(p_full, j & 1))) break;
-      tc_fence_after();
-      if (elect_one()) mma_ts<C::QB, 64>(tV, tS, make_desc(stage(j) + C::TILE, C::CH, 1024), idG, C::QB, j > 0);
-      __syncwarp();
-      if (j + 1 < n) scores(j + 1);
-      if (!(ok = ok && warp_wait(ds_full, j & 1))) break;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_ts<C::QB, 64>(tK, tP, make_desc(stage(j), C::CH, 1024), idG, C::QB, j > 0);
-        umma_commit(j + 1 < n ? &q_empty[j % C::NS] : done);
+    for (int seg = 0; ok && my.next(sp); ++seg) {
+      if (!(ok = warp_wait(kv_full, seg & 1))) break;
+      scores(jj);
+      dprobs(jj);
+      for (int j = my.i0; j < my.i1 && ok; ++j, ++jj) {
+        const bool more = j + 1 < my.i1;
+        if (more) {
+          if (!(ok = warp_wait(s_free, jj & 1))) break;
+          scores(jj + 1);
+        }
+        // dS and P are written; with a tile's first item its threads have also read the last tile's dV and dK
+        if (!(ok = ok && warp_wait(ds_full, jj & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_ts<C::QB, 32>(tV, tP + 16, make_desc(o_at(jj), C::CH, 1024), idG, C::QB, j > my.i0);
+          umma_commit(&o_empty[jj % C::NO]);
+          mma_ts<C::QB, 32>(tK, tP, make_desc(q_at(jj), C::CH, 1024), idG, C::QB, j > my.i0);
+          umma_commit(&q_empty[jj % C::NQ]);
+          if (!more) umma_commit(done);
+        }
+        __syncwarp();
+        if (more) dprobs(jj + 1);
       }
-      __syncwarp();
-      if (j + 1 < n) dprobs(j + 1);
     }
   } else {
     const int half = (int)(threadIdx.x - 64) >> 7;
-    const int r = (warp & 3) * 32 + lane, key = k0 + r;
+    const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tX = tS + half * 64 + lanes, tY = tP + half * 64 + lanes;
     const uint64_t sl = f2(p.scale * kLog2e, p.scale * kLog2e);
-    bool ok = true;
-    for (int j = 0; j < n && ok; ++j) {
-      const int q = query(j);
-      if (!(ok = warp_wait(&q_full[j % C::NS], (j / C::NS) & 1) && warp_wait(s_full, j & 1))) break;
-      tc_fence_after();
-      // lse and D of this thread's 64 queries
-      const float4* lse = reinterpret_cast<const float4*>(sQ + j % C::NS * C::STAGE + 2 * C::TILE) + half * 16;
-      const float4* del = lse + C::QB / 4;
-      float x[64], y[64];
-      uint32_t w[32];
-      tmem_row<64>(x, tX);
+    for (int seg = 0; ok && my.next(sp); ++seg) {
+      const int k0 = my.kb * kQB, key = k0 + r;
+      int qb = my.i0 % my.nqb;
+      for (int j = my.i0; j < my.i1; ++j, ++jj) {
+        const int q = k0 + qb * C::QB;
+        if (!(ok = warp_wait(&q_full[jj % C::NQ], (jj / C::NQ) & 1) && warp_wait(s_full, jj & 1))) break;
+        tc_fence_after();
+        // lse and D of this thread's 64 queries
+        const float4* lse = reinterpret_cast<const float4*>(sL + jj % C::NQ * C::QB) + half * 16;
+        const float4* del = reinterpret_cast<const float4*>(sD + jj % C::NO * C::QB) + half * 16;
+        float x[64];
+        tmem_row<64>(x, tX);
+        tc_fence_before();
+        mbar_arrive(s_free);
 #pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        const float4 l4 = lse[c / 4];
-        ex2_of(c / 2, fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
-        ex2_of(c / 2 + 1, fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
-      }
-      if (!all_visible(q, C::QB, k0, kQB, p.window, p.sinks)) {
-        const uint64_t vis = visible_queries(key, q + half * 64, p.window, p.sinks);
-        const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
+        for (int c = 0; c < 64; c += 4) {
+          const float4 l4 = lse[c / 4];
+          ex2_of(c / 2, fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
+          ex2_of(c / 2 + 1, fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
+        }
+        if (!all_visible(q, C::QB, k0, kQB, p.window, p.sinks)) {
+          const uint64_t vis = visible_queries(key, q + half * 64, p.window, p.sinks);
+          const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (!(bits[c / 32] >> (c % 32) & 1)) x[c] = 0.f;
-      }
+          for (int c = 0; c < 64; ++c)
+            if (!(bits[c / 32] >> (c % 32) & 1)) x[c] = 0.f;
+        }
+        if (!(ok = warp_wait(&o_full[jj % C::NO], (jj / C::NO) & 1) && warp_wait(dp_full, jj & 1))) break;
+        tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < 32; ++c) w[c] = pack2(x[2 * c], x[2 * c + 1]);
-      tmem_st16(tX, w);
-      tmem_st16(tX + 16, w + 16);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(p_full);
-      if (!(ok = warp_wait(dp_full, j & 1))) break;
-      tc_fence_after();
-      tmem_row<64>(y, tY);
-#pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        const float4 d4 = del[c / 4];
-        float a0, a1, a2, a3;
-        unpack(mul2(f2(x[c], x[c + 1]), add2(f2(y[c], y[c + 1]), f2(-d4.x, -d4.y))), a0, a1);
-        unpack(mul2(f2(x[c + 2], x[c + 3]), add2(f2(y[c + 2], y[c + 3]), f2(-d4.z, -d4.w))), a2, a3);
-        w[c / 2] = pack2(a0, a1);
-        w[c / 2 + 1] = pack2(a2, a3);
-      }
-      tmem_st16(tY, w);
-      tmem_st16(tY + 16, w + 16);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(ds_full);
-    }
-    ok = ok && warp_wait(done, 0);
-    if (ok) {
-      tc_fence_after();
-      if (np == 1) {  // K's and V's shared memory takes the tiles of dK and dV
-        float x0[HD / 4], x1[HD / 4];
-        tmem_row<HD / 4>(x0, tK + half * (HD / 4) + lanes);
-        tmem_row<HD / 4>(x1, tK + half * (HD / 4) + HD / 2 + lanes);
-        stage_grad<HD>(sK, C::CH, r, x0, x1, p, key, half);
-        if (HD == 128 || half == 0) {
-          float v[64];
+        for (int g = 0; g < 64; g += 32) {  // 32 queries' dP make room for 16 columns of dS and 16 of P
+          float y[32];
           uint32_t w[32];
-          tmem_row<64>(v, tV + half * 64 + lanes);
+          tmem_row<32>(y, tY + g);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1]);
-          stage_row(sV + half * C::CH, r, w);
+          for (int c = 0; c < 32; c += 4) {
+            const float4 d4 = del[(g + c) / 4];
+            const float* v = x + g + c;
+            float a0, a1, a2, a3;
+            unpack(mul2(f2(v[0], v[1]), add2(f2(y[c], y[c + 1]), f2(-d4.x, -d4.y))), a0, a1);
+            unpack(mul2(f2(v[2], v[3]), add2(f2(y[c + 2], y[c + 3]), f2(-d4.z, -d4.w))), a2, a3);
+            w[c / 2] = pack2(a0, a1);
+            w[c / 2 + 1] = pack2(a2, a3);
+            w[16 + c / 2] = pack2(v[0], v[1]);
+            w[16 + c / 2 + 1] = pack2(v[2], v[3]);
+          }
+          tmem_st32(tY + g, w);
         }
-        fence_proxy_async();
-      } else {  // [key row][dK, dV]
-        const int64_t at = (int64_t)bk * joined_parts(sp) + (sink || sp.ps == 1 ? y : (int64_t)sp.nsb * sp.ps + y);
-        float* dst = parts + (at * kQB + r) * (2 * HD) + half * HD;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(ds_full);
+        if (++qb == my.nqb) qb = 0;
+      }
+      const bool all = my.all(sp);
+      // a wait that runs out is shared at the barrier below, which every warp reaches
+      if ((ok = ok && warp_wait(done, seg & 1))) {
+        tc_fence_after();
+        if (!all && warp == 2 && elect_one()) mbar_arrive(kv_free);
+        if (all) {  // K's and V's shared memory takes the tiles of dK and dV
+          float x0[HD / 4], x1[HD / 4];
+          tmem_row<HD / 4>(x0, tK + half * (HD / 4) + lanes);
+          tmem_row<HD / 4>(x1, tK + half * (HD / 4) + HD / 2 + lanes);
+          stage_grad<HD>(sK, C::CH, r, x0, x1, p, key, half);
+          if (HD == 128 || half == 0) {
+            float v[64];
+            uint32_t w[32];
+            tmem_row<64>(v, tV + half * 64 + lanes);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1]);
+            stage_row(sV + half * C::CH, r, w);
+          }
+          fence_proxy_async();
+        } else {
+          float4* dst = reinterpret_cast<float4*>(parts) + part_at<HD>(blockIdx.x, my.i0 == 0, half, 0) + r;
 #pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          float v[32];
-          tmem_row<32>(v, (half ? tV : tK) + c + lanes);
+          for (int c = 0; c < HD; c += 32) {
+            float v[32];
+            tmem_row<32>(v, (half ? tV : tK) + c + lanes);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(dst + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            for (int e = 0; e < 8; ++e) dst[(c / 4 + e) * kQB] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
         }
       }
-    }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (warp == 2 && ok && np == 1 && elect_one()) {
+      if (!(ok = sync_all(1, 256, ok))) break;
+      if (all && warp == 2 && elect_one()) {
+        const int b = my.bk / p.hkv, kvh = my.bk % p.hkv;
 #pragma unroll
-      for (int c = 0; c < HD / 64; ++c) {
-        tma_store_3d(&tmDk, sK + c * C::CH, kvh * HD + c * 64, k0, b);
-        tma_store_3d(&tmDv, sV + c * C::CH, kvh * HD + c * 64, k0, b);
+        for (int c = 0; c < HD / 64; ++c) {
+          tma_store_3d(&tmDk, sK + c * C::CH, kvh * HD + c * 64, k0, b);
+          tma_store_3d(&tmDv, sV + c * C::CH, kvh * HD + c * 64, k0, b);
+        }
+        tma_store_wait();
+        mbar_arrive(kv_free);
       }
-      tma_store_wait();
+      __syncwarp();
     }
   }
   __syncwarp();
@@ -1105,103 +1196,65 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   }
 }
 
-// Adds the parts of a key row in order: a warp a row of dK and dV, its lanes over pairs of columns (c, c + HD / 2).
-// Parts without items were not written. Grid: [joined tiles x 16] x [B hkv], 8 rows a CTA.
+// Adds the parts of a cut tile in order: a warp takes 32 rows, 8 columns of dK or dV and their 8 rotary partners.
+// Grid: HD / 16 CTAs for each border between two shares; the first one that cuts a tile stands for it.
 template <int HD>
-__global__ void __launch_bounds__(256) k_window_join(const WinBwdArgs p, const Split sp, const float* __restrict__ parts,
-                                                     int kb0) {
+__global__ void __launch_bounds__(256) k_window_join(const WinBwdArgs p, const Split sp, const float* __restrict__ parts) {
+  const int cut = 1 + (int)blockIdx.x / (HD / 16), o = (int)blockIdx.x % (HD / 16) * 8, warp = threadIdx.x >> 5;
+  const int64_t v = sp.start(cut);
+  const TilePos at(sp, v);
+  const int dv = warp >> 2, r = (warp & 3) * 32 + (threadIdx.x & 31);
+  const int b = at.bk / p.hkv, kvh = at.bk % p.hkv, key = at.kb * kQB + r;
   pdl_wait();
   pdl_trigger();
-  const int kb = kb0 + (int)blockIdx.x / 16, r = ((int)blockIdx.x % 16) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int bk = blockIdx.y, b = bk / p.hkv, kvh = bk % p.hkv, key = kb * kQB + r;
-  if (key >= p.S) return;
-  const bool sink = kb < sp.nsb;
-  const int np = sink ? sp.ps : sp.pw;
-  const int64_t at = (int64_t)bk * joined_parts(sp) + (sink ? (int64_t)kb * np : (sp.ps > 1 ? (int64_t)sp.nsb * sp.ps : 0) + (int64_t)(kb - sp.nsb) * np);
-  const int64_t total = (int64_t)(p.hq / p.hkv) * sp.blocks(kb);
-  constexpr int N = HD / 64;  // pairs of columns a lane
-  float2 k1[N] = {}, v1[N] = {};
-  for (int i = 0; i < np; ++i) {
-    if (total * i / np == total * (i + 1) / np) continue;
-    const float* src = parts + ((at + i) * kQB + r) * (2 * HD);
+  if (v <= at.first || sp.start(cut - 1) > at.first || key >= p.S) return;
+  const int64_t end = at.first + (int64_t)sp.grp * sp.blocks(at.kb);
+  float lo[8] = {}, hi[8] = {};
+  for (int c = cut - 1; c < sp.ctas && sp.start(c) < end; ++c) {
+    const float4* src = reinterpret_cast<const float4*>(parts) + part_at<HD>(c, c < cut, dv, o) + r;
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-      const int o = lane + 32 * c;
-      k1[c].x += src[o];
-      k1[c].y += src[o + HD / 2];
-      v1[c].x += src[HD + o];
-      v1[c].y += src[HD + o + HD / 2];
+    for (int e = 0; e < 2; ++e) {
+      const float4 x = src[e * kQB], y = src[(HD / 8 + e) * kQB];
+      lo[4 * e] += x.x, lo[4 * e + 1] += x.y, lo[4 * e + 2] += x.z, lo[4 * e + 3] += x.w;
+      hi[4 * e] += y.x, hi[4 * e + 1] += y.y, hi[4 * e + 2] += y.z, hi[4 * e + 3] += y.w;
     }
   }
-  const int64_t t = (int64_t)b * p.S + key;
+  if (!dv) {
 #pragma unroll
-  for (int c = 0; c < N; ++c) {
-    const int o = lane + 32 * c;
-    float y1 = k1[c].x * p.scale, y2 = k1[c].y * p.scale;
-    if (p.rope_cos) {
-      const float cs = p.rope_cos[(int64_t)key * (HD / 2) + o], sn = p.rope_sin[(int64_t)key * (HD / 2) + o];
-      const float z = y1 * cs + y2 * sn;
-      y2 = y2 * cs - y1 * sn;
-      y1 = z;
-    }
-    __nv_bfloat16* dk = p.dk + t * p.lddk + (int64_t)kvh * HD;
-    __nv_bfloat16* dv = p.dv + t * p.lddv + (int64_t)kvh * HD;
-    dk[o] = __float2bfloat16_rn(y1);
-    dk[o + HD / 2] = __float2bfloat16_rn(y2);
-    dv[o] = __float2bfloat16_rn(v1[c].x);
-    dv[o + HD / 2] = __float2bfloat16_rn(v1[c].y);
-  }
-}
-
-// How the dK / dV work is cut, by the estimated time in blocks: a CTA costs about 3 besides its own (start,
-// tiles of K and V, stores), the joining kernel about 5, and the CTAs that do not all start at once end on
-// average half a CTA after the SMs' mean (the tiles with sinks, the longest, start first).
-Split make_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
-  constexpr int sms = 148;
-  const int64_t units = T / S * hkv;
-  const int grp = hq / hkv;
-  Split s;
-  s.nkb = (S + kQB - 1) / kQB;
-  s.nsb = (int)(((int64_t)std::min(sinks, S) + kQB - 1) / kQB);
-  s.nq = s.nkb;
-  s.near = (int)std::min<int64_t>(s.nq, ((int64_t)kQB - 2 + std::min(window, S)) / kQB + 1);
-  const int64_t tw = (int64_t)grp * s.near, ts = (int64_t)grp * s.nq;  // of the longest tiles
-  int64_t work = 0;
-  for (int kb = 0; kb < s.nkb; ++kb) work += (int64_t)grp * s.blocks(kb);
-  double best = 0;
-  int bs = 0, bw = 0;
-  for (int pw = 1; pw <= 16 && (pw == 1 || tw / pw >= 2); ++pw) {
-    for (int64_t ps = 1; s.nsb > 0 ? ps <= 256 && (ps == 1 || ts / ps >= 2) : ps == 1; ps += ps < 16 ? 1 : ps / 8) {
-      s.ps = (int)ps;
-      s.pw = pw;
-      const int64_t ctas = units * s.ctas();
-      const int64_t len = std::max(s.nsb < s.nkb ? (tw + pw - 1) / pw : 0, s.nsb > 0 ? (ts + ps - 1) / ps : 0) + 3;
-      double cost = ctas <= sms ? (double)len : std::max((double)len, (double)(units * work + 3 * ctas) / sms + 0.5 * len);
-      if (joined_parts(s) > 0) cost += 5;
-      if (bw == 0 || cost < best) {
-        best = cost;
-        bs = (int)ps;
-        bw = pw;
+    for (int e = 0; e < 8; ++e) {
+      lo[e] *= p.scale;
+      hi[e] *= p.scale;
+      if (p.rope_cos) {
+        const int64_t t = (int64_t)key * (HD / 2) + o + e;
+        const float cs = p.rope_cos[t], sn = p.rope_sin[t], z = lo[e] * cs + hi[e] * sn;
+        hi[e] = hi[e] * cs - lo[e] * sn;
+        lo[e] = z;
       }
     }
   }
-  s.ps = bs;
-  s.pw = bw;
-  return s;
+  __nv_bfloat16* out = (dv ? p.dv : p.dk) + ((int64_t)b * p.S + key) * (dv ? p.lddv : p.lddk) + (int64_t)kvh * HD + o;
+  *reinterpret_cast<uint4*>(out) = make_uint4(pack2(lo[0], lo[1]), pack2(lo[2], lo[3]), pack2(lo[4], lo[5]), pack2(lo[6], lo[7]));
+  *reinterpret_cast<uint4*>(out + HD / 2) = make_uint4(pack2(hi[0], hi[1]), pack2(hi[2], hi[3]), pack2(hi[4], hi[5]), pack2(hi[6], hi[7]));
 }
-// The same, kept for a thread's next call: a model's layers ask for the same sizes.
-Split plan_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
-  struct Key {
-    int64_t T;
-    int S, hq, hkv, window, sinks;
-  };
-  static thread_local Key last{0, 0, 0, 0, 0, 0};
-  static thread_local Split split;
-  if (last.T != T || last.S != S || last.hq != hq || last.hkv != hkv || last.window != window || last.sinks != sinks) {
-    split = make_split(T, S, hq, hkv, window, sinks);
-    last = Key{T, S, hq, hkv, window, sinks};
-  }
-  return split;
+
+// How the dK / dV work is cut. Whole tiles where there are as few as the SMs and the longest of them
+// takes no longer than equal shares and the kernel that joins them (about kJoin items).
+constexpr int kJoin = 4;
+Split make_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
+  constexpr int sms = 148;
+  const int64_t units = T / S * hkv;
+  Split s;
+  s.nkb = (S + kQB - 1) / kQB;
+  s.nsb = (int)(((int64_t)std::min(sinks, S) + kQB - 1) / kQB);
+  s.near = (int)std::min<int64_t>(s.nkb, ((int64_t)kQB - 2 + std::min(window, S)) / kQB + 1);
+  s.grp = hq / hkv;
+  s.unit = s.before(s.nkb);
+  s.total = units * s.unit;
+  const int64_t tiles = units * s.nkb, items = s.total - kSeg * tiles;
+  s.ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(1, items / 2));
+  s.whole = tiles <= sms && (int64_t)s.grp * s.blocks(0) + kSeg <= s.total / s.ctas + kJoin;
+  if (s.whole) s.ctas = (int)tiles;
+  return s;
 }
 
 // 3D map of a [B, S, cols] bf16 tensor with row stride ld: boxes of `rows` rows x 64 columns, 128-byte swizzle,
@@ -1264,15 +1317,13 @@ cudaError_t launch_bwd(const WinBwdArgs& a, cudaStream_t s) {
                v16, dq, fo, a, tiles);
   note_launch(1);
   if (e != cudaSuccess) return e;
-  const Split sp = plan_split(a.T, a.S, a.hq, a.hkv, a.window, a.sinks);
+  const Split sp = make_split(a.T, a.S, a.hq, a.hkv, a.window, a.sinks);
   float* parts = a.D + 2 * B * a.hq * up(a.S, kQB);
-  e = launch_k(k_window_dkdv<HD>, dim3((unsigned)(B * a.hkv * sp.ctas())), dim3(320), K::SMEM, s, 0, q, o, k, v, dk, dv, a, sp,
+  e = launch_k(k_window_dkdv<HD>, dim3((unsigned)sp.ctas), dim3(320), K::SMEM, s, 0, q, o, k, v, dk, dv, a, sp,
                parts);
   note_launch(1);
-  if (e != cudaSuccess || joined_parts(sp) == 0) return e;
-  const int kb0 = sp.nsb > 0 && sp.ps > 1 ? 0 : sp.nsb, kb1 = sp.pw > 1 ? sp.nkb : sp.nsb;
-  e = launch_k(k_window_join<HD>, dim3((unsigned)((kb1 - kb0) * 16), (unsigned)(B * a.hkv)), dim3(256), 0, s, 0, a, sp,
-               static_cast<const float*>(parts), kb0);
+  if (e != cudaSuccess || sp.whole || sp.ctas == 1) return e;
+  e = launch_k(k_window_join<HD>, dim3((unsigned)(sp.ctas - 1) * (HD / 16)), dim3(256), 0, s, 0, a, sp, static_cast<const float*>(parts));
   note_launch(1);
   return e;
 }
@@ -1285,8 +1336,8 @@ bool window_shape_ok(int64_t T, int S, int hq, int hkv, int hd, int window, int 
 }
 
 int64_t window_scratch(int64_t T, int S, int hq, int hkv, int hd, int window, int sinks) {
-  const Split sp = plan_split(T, S, hq, hkv, std::min(window, S), std::min(sinks, S));
-  return T / S * (2 * (int64_t)hq * up(S, kQB) + hkv * joined_parts(sp) * kQB * 2 * hd);
+  const Split sp = make_split(T, S, hq, hkv, std::min(window, S), std::min(sinks, S));
+  return T / S * 2 * hq * up(S, kQB) + (sp.whole || sp.ctas == 1 ? 0 : (int64_t)sp.ctas * 2 * kQB * 2 * hd);
 }
 
 cudaError_t window_fwd(WinArgs a, cudaStream_t s) {
