@@ -173,6 +173,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return done;
 }
 
+// the same for three barriers at once
+__device__ __forceinline__ bool warp_wait3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) {
+  bool done = false;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kSpinLimit && !done; ++i) {
+    const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb), z = mbar_try_wait(c, pc);
+    done = __all_sync(0xffffffffu, x && y && z);
+  }
+  if (!done) dev_fail(DEV_ERR_MBAR_TIMEOUT);
+  return done;
+}
+
 __host__ __device__ __forceinline__ int up(int a, int b) { return (a + b - 1) / b * b; }
 
 // The key blocks that the queries [q0, q0 + 128) of a sequence see, in order: sinks in front of the
@@ -851,78 +863,55 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
 }
 
 // ---------------------------------------------------------------------------------- dK, dV
-// An item is 128 keys of a kv head against 128 queries of one of its heads. The items lie in a row: by sequence and
-// kv head (a unit), by key tile, by head, by query block. Each of the CTAs takes an equal share of the row, its cuts
-// in fixed places; what a tile costs besides its items (K, V, the stores) counts as kSeg items in front of
-// it, which also moves cuts next to a tile's border onto the border. The sums of a tile in one share are stored as dK and dV;
-// those of a cut tile go to the scratch as fp32, where k_window_join adds them in order. With few tiles
-// each is a CTA of its own (whole).
+// An item is 128 keys of a kv head against 128 queries of one of its heads; the items of a key tile lie by head, by
+// query block. The tiles lie in a row, by sequence and kv head (a unit), those that hold sinks, whose
+// queries reach to the sequence's end, behind all others. Of its front each CTA takes every ctas-th tile whole, so that
+// the CTAs at work are on neighbouring tiles, which share most of Q and dO (with neighbouring tiles in one
+// CTA instead, 685 MB came from HBM for 9472 tokens rather than 196, and the kernel took 10 % longer);
+// the rest is cut, at fixed places, to make the CTAs' work equal. What a tile costs besides its items (K, V, the
+// stores) counts as kSeg items in front of them, which also moves cuts next to a tile's border onto the
+// border. The sums of a cut tile's parts go to the scratch as fp32, where k_window_join adds them in order.
+constexpr int kSms = 148, kSeg = 2;
 struct Split {
-  int nkb, nsb;   // key tiles of a sequence, those that hold sinks
-  int near;       // query blocks that see a tile through the window
-  int grp;        // heads of a kv head
-  int ctas, whole;
-  int64_t unit, total;  // length of a unit, of the row
-  // query blocks that see a key tile; all of the items in front of it in its unit
-  __host__ __device__ int blocks(int kb) const {
+  int nkb, nsb;  // key tiles of a sequence, those that hold sinks
+  int near;      // query blocks that see a tile through the window
+  int grp;       // heads of a kv head
+  int plain;     // tiles without sinks, of all units
+  int ctas, rounds;  // each CTA's whole tiles
+  int tile[kSms + 1], off[kSms + 1];  // CTA c's share of the rest: from place off[c] of tile[c] to off[c + 1] of tile[c + 1]
+  __host__ __device__ int blocks(int kb) const {  // query blocks that see a key tile
     const int n = nkb - kb;
     return kb < nsb || n < near ? n : near;
   }
-  __host__ __device__ int64_t before(int kb) const;
-  __host__ __device__ int64_t start(int c) const {
-    return whole ? c / nkb * unit + before(c % nkb) : total * c / ctas;
+  __host__ __device__ void locate(int t, int& bk, int& kb) const {  // unit and key tile of the row's tile t
+    const int n = t < plain ? nkb - nsb : nsb, u = t < plain ? t : t - plain;
+    bk = u / n;
+    kb = u % n + (t < plain ? nsb : 0);
   }
+  __host__ __device__ bool cut(int c) const { return off[c] > kSeg; }  // border c lies inside of tile[c]'s items
 };
-constexpr int kSeg = 2;
-__host__ __device__ inline int64_t Split::before(int kb) const {
-  const auto falling = [&](int64_t k0, int64_t k1) { return k1 > k0 ? (k1 - k0) * (2 * (int64_t)nkb - k0 - k1 + 1) / 2 : 0; };
-  const int knee = nkb - near > nsb ? nkb - near : nsb;  // tiles from here on are seen to the sequence's end
-  int64_t n = falling(0, kb < nsb ? kb : nsb);
-  if (kb > nsb) n += (int64_t)near * ((kb < knee ? kb : knee) - nsb) + falling(knee, kb);
-  return n * grp + (int64_t)kSeg * kb;
-}
-// The tile that place v of the row lies in.
-struct TilePos {
-  int bk, kb;
-  int64_t first;  // place of its first item
-  __device__ __forceinline__ TilePos(const Split& sp, int64_t v) {
-    bk = (int)(v / sp.unit);
-    const int64_t r = v - bk * sp.unit;
-    int lo = 0, hi = sp.nkb - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (sp.before(mid) <= r) lo = mid;
-      else hi = mid - 1;
-    }
-    kb = lo;
-    first = bk * sp.unit + sp.before(kb) + kSeg;
-  }
-};
-// A CTA's share, tile by tile: items [i0, i1) of key tile kb of unit bk, seen by nqb query blocks. What it keeps
-// between tiles is little, 32 bits each: the kernel's threads have no registers to spare.
+// A CTA's tiles: items [i0, i1) of key tile kb of unit bk, seen by nqb query blocks.
 struct Share {
-  int first, end;  // the next tile's first item, the share's end, counted from the share's start
-  int bk, kb;      // this tile's (before the first: in front of its tile)
-  int nqb, i0, i1;
-  __device__ __forceinline__ Share(const Split& sp, int c) {
-    const int64_t v = sp.start(c);
-    const TilePos at(sp, v);
-    first = (int)(at.first - v);
-    end = (int)(sp.start(c + 1) - v);
-    bk = at.bk;
-    kb = at.kb - 1;
-  }
+  int round, t;  // the next round, or tile of the cut rest
+  int bk, kb, nqb, i0, i1;
+  __device__ __forceinline__ Share() : round(0), t(-1) {}
   __device__ __forceinline__ bool next(const Split& sp) {
-    while (first < end) {
-      if (++kb == sp.nkb) {
-        kb = 0;
-        ++bk;
-      }
+    const int c = blockIdx.x;
+    if (round < sp.rounds) {
+      sp.locate(c + sp.ctas * round++, bk, kb);
       nqb = sp.blocks(kb);
-      const int len = sp.grp * nqb;
-      i0 = max(-first, 0);
-      i1 = min(end - first, len);
-      first += len + kSeg;
+      i0 = 0;
+      i1 = sp.grp * nqb;
+      return true;
+    }
+    if (t < 0) t = sp.tile[c];
+    while (t <= sp.tile[c + 1]) {
+      const bool head = t == sp.tile[c], tail = t == sp.tile[c + 1];
+      if (tail && !sp.cut(c + 1)) break;
+      sp.locate(t++, bk, kb);
+      nqb = sp.blocks(kb);
+      i0 = head ? max(sp.off[c] - kSeg, 0) : 0;
+      i1 = tail ? sp.off[c + 1] - kSeg : sp.grp * nqb;
       if (i1 > i0) return true;
     }
     return false;
@@ -951,8 +940,9 @@ struct DkvCfg {
 //   dV += P^T dO, dK += dS^T Q with P^T and dS^T, as bf16 side by side over dP^T in TMEM, as A operands
 // (Q and dO read MN-major from the tiles used K-major for the scores). With dV, dK and both scores TMEM is
 // full; with K, V, three blocks of Q and two of dO shared memory is, too. P waits in registers for dP, so
-// that S of j + 1 is issued once the threads have read S of j, and dV and dK of j and dP of j + 1 run under the
-// exponentials of j + 1.
+// that S of j + 1 is issued behind dP of j, and dV and dK of j, dP of j + 1 and S of j + 2 run under the
+// threads' work on j + 1. The products of an item are issued in two runs, since the tensor cores' queue is short: a
+// wait between each two of the four left them idle for 1000 clocks of the 3600 that an item then took.
 template <int HD>
 __global__ void __launch_bounds__(320, 1)
 k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
@@ -995,7 +985,7 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot), tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
-  Share my(sp, blockIdx.x);
+  Share my;
   pdl_wait();
   pdl_trigger();
 
@@ -1040,48 +1030,52 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     }
   } else if (warp == 1) {
     constexpr uint32_t idS = umma_idesc_bf16(128, C::QB, 0, 0), idG = umma_idesc_bf16(128, HD, 0, 1);
-    const auto q_at = [&](int j) { return smem_u32(sQ + j % C::NQ * C::TILE); };
-    const auto o_at = [&](int j) { return smem_u32(sO + j % C::NO * C::TILE); };
-    const auto scores = [&](int j) {  // S^T_j = K Q_j^T
-      if (!(ok = ok && warp_wait(&q_full[j % C::NQ], (j / C::NQ) & 1))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_ss<HD>(tS, make_desc(smem_u32(sK), 16, 1024), C::CH, make_desc(q_at(j), 16, 1024), C::CH, idS);
-        umma_commit(s_full);
-      }
-      __syncwarp();
-    };
-    const auto dprobs = [&](int j) {  // dP^T_j = V dO_j^T
-      if (!(ok = ok && warp_wait(&o_full[j % C::NO], (j / C::NO) & 1))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_ss<HD>(tP, make_desc(smem_u32(sV), 16, 1024), C::CH, make_desc(o_at(j), 16, 1024), C::CH, idS);
-        umma_commit(dp_full);
-      }
-      __syncwarp();
+    const Desc dK = make_desc(smem_u32(sK), 16, 1024), dV = make_desc(smem_u32(sV), 16, 1024);
+    const Desc qk = make_desc(smem_u32(sQ), 16, 1024), qm = make_desc(smem_u32(sQ), C::CH, 1024);  // K- and MN-major
+    const Desc ok_ = make_desc(smem_u32(sO), 16, 1024), om = make_desc(smem_u32(sO), C::CH, 1024);
+    // slots of the rings of Q and dO and the parities of their phases: of this item and, for Q, of the next
+    int sq = 0, so = 0;
+    uint32_t pq = 0, po = 0;
+    const auto scores = [&] {  // S^T = K Q^T
+      mma_ss<HD>(tS, dK, C::CH, at(qk, sq * C::TILE), C::CH, idS);
+      umma_commit(s_full);
     };
     for (int seg = 0; ok && my.next(sp); ++seg) {
-      if (!(ok = warp_wait(kv_full, seg & 1))) break;
-      scores(jj);
-      dprobs(jj);
-      for (int j = my.i0; j < my.i1 && ok; ++j, ++jj) {
-        const bool more = j + 1 < my.i1;
-        if (more) {
-          if (!(ok = warp_wait(s_free, jj & 1))) break;
-          scores(jj + 1);
+      if (!(ok = warp_wait(kv_full, seg & 1) && warp_wait(&q_full[sq], pq))) break;
+      tc_fence_after();
+      if (elect_one()) scores();
+      __syncwarp();
+      bool add = false;
+      for (int n = my.i1 - my.i0; n > 0; --n, ++jj) {
+        const int q0 = sq;
+        if (++sq == C::NQ) {
+          sq = 0;
+          pq ^= 1;
         }
-        // dS and P are written; with a tile's first item its threads have also read the last tile's dV and dK
-        if (!(ok = ok && warp_wait(ds_full, jj & 1))) break;
+        if (!(ok = n > 1 ? warp_wait3(&o_full[so], po, s_free, jj & 1, &q_full[sq], pq) : warp_wait(&o_full[so], po))) break;
         tc_fence_after();
-        if (elect_one()) {
-          mma_ts<C::QB, 32>(tV, tP + 16, make_desc(o_at(jj), C::CH, 1024), idG, C::QB, j > my.i0);
-          umma_commit(&o_empty[jj % C::NO]);
-          mma_ts<C::QB, 32>(tK, tP, make_desc(q_at(jj), C::CH, 1024), idG, C::QB, j > my.i0);
-          umma_commit(&q_empty[jj % C::NQ]);
-          if (!more) umma_commit(done);
+        if (elect_one()) {  // dP^T = V dO^T, and the next item's scores
+          mma_ss<HD>(tP, dV, C::CH, at(ok_, so * C::TILE), C::CH, idS);
+          umma_commit(dp_full);
+          if (n > 1) scores();
         }
         __syncwarp();
-        if (more) dprobs(jj + 1);
+        // dS and P are written; with a tile's first item its threads have also read the last tile's dV and dK
+        if (!(ok = warp_wait(ds_full, jj & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_ts<C::QB, 32>(tV, tP + 16, at(om, so * C::TILE), idG, C::QB, add);
+          umma_commit(&o_empty[so]);
+          mma_ts<C::QB, 32>(tK, tP, at(qm, q0 * C::TILE), idG, C::QB, add);
+          umma_commit(&q_empty[q0]);
+          if (n == 1) umma_commit(done);
+        }
+        __syncwarp();
+        add = true;
+        if (++so == C::NO) {
+          so = 0;
+          po ^= 1;
+        }
       }
     }
   } else {
@@ -1199,18 +1193,20 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 // Adds the parts of a cut tile in order: a warp takes 32 rows, 8 columns of dK or dV and their 8 rotary partners.
 // Grid: HD / 16 CTAs for each border between two shares; the first one that cuts a tile stands for it.
 template <int HD>
-__global__ void __launch_bounds__(256) k_window_join(const WinBwdArgs p, const Split sp, const float* __restrict__ parts) {
+__global__ void __launch_bounds__(256) k_window_join(const WinBwdArgs p, const __grid_constant__ Split sp,
+                                                     const float* __restrict__ parts) {
   const int cut = 1 + (int)blockIdx.x / (HD / 16), o = (int)blockIdx.x % (HD / 16) * 8, warp = threadIdx.x >> 5;
-  const int64_t v = sp.start(cut);
-  const TilePos at(sp, v);
   const int dv = warp >> 2, r = (warp & 3) * 32 + (threadIdx.x & 31);
-  const int b = at.bk / p.hkv, kvh = at.bk % p.hkv, key = at.kb * kQB + r;
   pdl_wait();
   pdl_trigger();
-  if (v <= at.first || sp.start(cut - 1) > at.first || key >= p.S) return;
-  const int64_t end = at.first + (int64_t)sp.grp * sp.blocks(at.kb);
+  if (!sp.cut(cut) || (sp.tile[cut - 1] == sp.tile[cut] && sp.cut(cut - 1))) return;
+  int bk, kb;
+  sp.locate(sp.tile[cut], bk, kb);
+  const int b = bk / p.hkv, kvh = bk % p.hkv, key = kb * kQB + r;
+  if (key >= p.S) return;
   float lo[8] = {}, hi[8] = {};
-  for (int c = cut - 1; c < sp.ctas && sp.start(c) < end; ++c) {
+  for (int c = cut - 1; c < cut || (c < sp.ctas && sp.tile[c] == sp.tile[cut]); ++c) {
+    if (c >= cut && sp.tile[c + 1] == sp.tile[c] && sp.off[c + 1] == sp.off[c]) continue;  // an empty share
     const float4* src = reinterpret_cast<const float4*>(parts) + part_at<HD>(c, c < cut, dv, o) + r;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -1237,24 +1233,74 @@ __global__ void __launch_bounds__(256) k_window_join(const WinBwdArgs p, const S
   *reinterpret_cast<uint4*>(out + HD / 2) = make_uint4(pack2(hi[0], hi[1]), pack2(hi[2], hi[3]), pack2(hi[4], hi[5]), pack2(hi[6], hi[7]));
 }
 
-// How the dK / dV work is cut. Whole tiles where there are as few as the SMs and the longest of them
-// takes no longer than equal shares and the kernel that joins them (about kJoin items).
-constexpr int kJoin = 4;
+// How the dK / dV work is dealt out. As many rounds of whole tiles as leave no CTA with more than its share; where
+// the tiles are as few as the SMs, a CTA each, if the longest of them takes no longer than equal shares and the
+// stores and the kernel that join them (about kJoin items: 4 sequences of 512 tokens take 65 us in whole
+// tiles of up to 16 items, 69 us in shares of 8.6).
+constexpr int kJoin = 10;
 Split make_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
-  constexpr int sms = 148;
   const int64_t units = T / S * hkv;
   Split s;
   s.nkb = (S + kQB - 1) / kQB;
   s.nsb = (int)(((int64_t)std::min(sinks, S) + kQB - 1) / kQB);
   s.near = (int)std::min<int64_t>(s.nkb, ((int64_t)kQB - 2 + std::min(window, S)) / kQB + 1);
   s.grp = hq / hkv;
-  s.unit = s.before(s.nkb);
-  s.total = units * s.unit;
-  const int64_t tiles = units * s.nkb, items = s.total - kSeg * tiles;
-  s.ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(1, items / 2));
-  s.whole = tiles <= sms && (int64_t)s.grp * s.blocks(0) + kSeg <= s.total / s.ctas + kJoin;
-  if (s.whole) s.ctas = (int)tiles;
+  s.plain = (int)(units * (s.nkb - s.nsb));
+  const int tiles = (int)(units * s.nkb);
+  const auto cost = [&](int t) {
+    int bk, kb;
+    s.locate(t, bk, kb);
+    return (int64_t)s.grp * s.blocks(kb) + kSeg;
+  };
+  int64_t total = 0;
+  for (int kb = 0; kb < s.nkb; ++kb) total += units * ((int64_t)s.grp * s.blocks(kb) + kSeg);
+  const int64_t items = total - (int64_t)kSeg * tiles;
+  s.ctas = (int)std::min<int64_t>(kSms, std::max<int64_t>(1, items / 2));
+  s.rounds = 0;
+  if (tiles <= kSms && (int64_t)s.grp * s.blocks(0) + kSeg <= total / s.ctas + kJoin) {
+    s.ctas = tiles;
+    s.rounds = 1;
+  }
+  int64_t own[kSms] = {};  // whole tiles of each CTA
+  if (s.rounds == 0) {
+    for (int64_t t = 0; t + s.ctas <= s.plain; t += s.ctas, ++s.rounds) {
+      bool fits = true;
+      for (int c = 0; c < s.ctas; ++c) fits = fits && own[c] + cost((int)t + c) <= total / s.ctas;
+      if (!fits) break;
+      for (int c = 0; c < s.ctas; ++c) own[c] += cost((int)t + c);
+    }
+  } else {
+    for (int c = 0; c < s.ctas; ++c) own[c] = cost(c);
+  }
+  int t = s.rounds * s.ctas;
+  int64_t at = 0;  // place in tile t
+  for (int c = 0; c <= s.ctas; ++c) {
+    while (t < tiles && (c == s.ctas || at >= cost(t))) at -= cost(t++);
+    s.tile[c] = t;
+    s.off[c] = t < tiles ? (int)at : 0;
+    if (c < s.ctas) at += std::max<int64_t>(0, total * (c + 1) / s.ctas - total * c / s.ctas - own[c]);
+  }
   return s;
+}
+// The same, kept for a thread's next call: a model's layers ask for the same sizes.
+const Split& plan_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
+  struct Key {
+    int64_t T;
+    int S, hq, hkv, window, sinks;
+  };
+  static thread_local Key last{0, 0, 0, 0, 0, 0};
+  static thread_local Split split;
+  if (last.T != T || last.S != S || last.hq != hq || last.hkv != hkv || last.window != window || last.sinks != sinks) {
+    split = make_split(T, S, hq, hkv, window, sinks);
+    last = Key{T, S, hq, hkv, window, sinks};
+  }
+  return split;
+}
+// parts that go to the scratch
+int64_t split_parts(const Split& s) {
+  for (int c = 1; c < s.ctas; ++c)
+    if (s.cut(c)) return 2 * (int64_t)s.ctas;
+  return 0;
 }
 
 // 3D map of a [B, S, cols] bf16 tensor with row stride ld: boxes of `rows` rows x 64 columns, 128-byte swizzle,
@@ -1317,12 +1363,12 @@ cudaError_t launch_bwd(const WinBwdArgs& a, cudaStream_t s) {
                v16, dq, fo, a, tiles);
   note_launch(1);
   if (e != cudaSuccess) return e;
-  const Split sp = make_split(a.T, a.S, a.hq, a.hkv, a.window, a.sinks);
+  const Split& sp = plan_split(a.T, a.S, a.hq, a.hkv, a.window, a.sinks);
   float* parts = a.D + 2 * B * a.hq * up(a.S, kQB);
   e = launch_k(k_window_dkdv<HD>, dim3((unsigned)sp.ctas), dim3(320), K::SMEM, s, 0, q, o, k, v, dk, dv, a, sp,
                parts);
   note_launch(1);
-  if (e != cudaSuccess || sp.whole || sp.ctas == 1) return e;
+  if (e != cudaSuccess || split_parts(sp) == 0) return e;
   e = launch_k(k_window_join<HD>, dim3((unsigned)(sp.ctas - 1) * (HD / 16)), dim3(256), 0, s, 0, a, sp, static_cast<const float*>(parts));
   note_launch(1);
   return e;
@@ -1336,8 +1382,8 @@ bool window_shape_ok(int64_t T, int S, int hq, int hkv, int hd, int window, int 
 }
 
 int64_t window_scratch(int64_t T, int S, int hq, int hkv, int hd, int window, int sinks) {
-  const Split sp = make_split(T, S, hq, hkv, std::min(window, S), std::min(sinks, S));
-  return T / S * 2 * hq * up(S, kQB) + (sp.whole || sp.ctas == 1 ? 0 : (int64_t)sp.ctas * 2 * kQB * 2 * hd);
+  const Split& sp = plan_split(T, S, hq, hkv, std::min(window, S), std::min(sinks, S));
+  return T / S * 2 * hq * up(S, kQB) + split_parts(sp) * kQB * 2 * hd;
 }
 
 cudaError_t window_fwd(WinArgs a, cudaStream_t s) {
