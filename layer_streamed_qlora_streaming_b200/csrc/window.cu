@@ -173,13 +173,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return done;
 }
 
-// the same for three barriers at once
-__device__ __forceinline__ bool warp_wait3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) {
+// the same for two barriers
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
   bool done = false;
 #pragma unroll 1
   for (uint32_t i = 0; i < kSpinLimit && !done; ++i) {
-    const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb), z = mbar_try_wait(c, pc);
-    done = __all_sync(0xffffffffu, x && y && z);
+    const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+    done = __all_sync(0xffffffffu, x && y);
   }
   if (!done) dev_fail(DEV_ERR_MBAR_TIMEOUT);
   return done;
@@ -606,23 +606,24 @@ __host__ __device__ __forceinline__ int64_t stat_row(int b, int h, int hq, int S
 }
 
 // ---------------------------------------------------------------------------------- dQ
-// Persistent CTAs, one an SM, taking the query tiles in turn; 320 threads: warp 0 TMA, warp 1 the MMAs, warps 2-9 two threads a query row
-// (half of a block's columns each); the next tile's Q, dO and o, two K blocks and one V block of 128 keys
-// are in flight.
+// Persistent CTAs, one an SM, taking the query tiles in turn; 320 threads: warp 0 TMA, warp 1 the MMAs, warps 2-9 two
+// threads a query row (half of a block's columns each); the next tile's Q, dO and o and up to three K
+// blocks and one V block of 128 keys are in flight.
 // Q and dO are copied into TMEM first and serve as the A operands from there: read from shared memory for
 // every block they took its whole bandwidth (128 bytes a clock: with K, V, their loads and dS K 1800
-// clocks a block, where the tensor cores take 1540), and their place is free for the next tile's.
-// S of block j + 1 is issued as soon as the threads have read S of j; dS goes over dP (bf16, the A operand
-// of dQ += dS K), and dP of j + 1 follows that product, under the exponentials of j + 1. (Blocks of 64 keys
-// with two buffers of each took 2060 clocks a block: at N = 64 the issue of an MMA takes longer than its
-// 32 clocks.) The tile of dQ leaves by TMA under the next tile. With a CTA a tile, its start (setup, Q,
-// dO, o) and end took 9500 clocks of the 31600 of a tile of ten blocks.
+// clocks a block, where the tensor cores take 1540), and their place is free for the next tile's. o, which
+// only D needs, passes through K's ring.
+// S of block j + 1 is issued right behind dP of j; dS goes over dP (bf16, the A operand of dQ += dS K), and dP of
+// j + 1 follows that product, under the exponentials of j + 1. (Blocks of 64 keys with two buffers of each
+// took 2060 clocks a block: at N = 64 the issue of an MMA takes longer than its 32 clocks.)
+// A tile's end overlaps the next one's start: Q and dO of the next tile go to TMEM before dQ leaves it, so that
+// the first products run under dQ's way out (by TMA, from shared memory).
 template <int HD>
 struct DqCfg {
-  static constexpr int KB = 128;  // keys of a block
+  static constexpr int KB = 128, NK = 3;  // keys of a block, blocks of K in flight
   static constexpr uint32_t CH = kQB * 128;
   static constexpr uint32_t TILE = (HD / 64) * CH;
-  static constexpr uint32_t SMEM = 7 * TILE + 1024 + 256 + kQB * 4;
+  static constexpr uint32_t SMEM = 7 * TILE + 1024 + 256 + 2 * kQB * 4;
 };
 
 template <int HD>
@@ -636,16 +637,15 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   constexpr int kKB = C::KB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sQ = smem, *sO = smem + C::TILE, *sF = smem + 2 * C::TILE, *sK = smem + 3 * C::TILE, *sV = smem + 5 * C::TILE,
-          *sG = smem + 6 * C::TILE;  // Q, dO, o, K [2], V, dQ on its way out
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 7 * C::TILE);
+  // Q, dO, K and o [NK], V, dQ on its way out
+  uint8_t *sQ = smem, *sO = sQ + C::TILE, *sK = sO + C::TILE, *sV = sK + C::NK * C::TILE, *sG = sV + C::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sG + C::TILE);
   uint64_t *a_full = bars, *s_free = bars + 1, *ds_full = bars + 2;  // of all 256 row threads
-  uint64_t *q_full = bars + 3, *s_full = bars + 4, *dp_full = bars + 5, *done = bars + 6;
-  uint64_t *k_full = bars + 7, *k_empty = bars + 9;  // [2]
-  uint64_t *v_full = bars + 11, *v_empty = bars + 12;
-  constexpr int kBars = 13;
+  uint64_t *q_full = bars + 3, *s_full = bars + 4, *dp_full = bars + 5, *done = bars + 6, *v_full = bars + 7,
+           *v_empty = bars + 8, *k_full = bars + 9, *k_empty = k_full + C::NK;
+  constexpr int kBars = 9 + 2 * C::NK;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
-  float* sD = reinterpret_cast<float*>(bars + kBars + 1);  // [128]
+  float* sD = reinterpret_cast<float*>(bars + kBars + 1);  // [2][128], by tile
   const int grp = p.hq / p.hkv;
   const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -673,77 +673,95 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
   pdl_wait();
   pdl_trigger();
 
-  // it counts the CTA's tiles, jj its blocks: barrier phases run on over the tiles
+  // it counts the CTA's tiles, jj its blocks: barrier phases run on over the tiles. K's ring holds o of a tile
+  // and then its blocks; slot and par: its next entry and the parity of that entry's phase.
+  bool ok = true;
+  int it = 0, jj = 0, slot = 0;
+  uint32_t par = 0;
+  const auto advance = [&](int n) {
+    slot += n;
+    while (slot >= C::NK) {
+      slot -= C::NK;
+      par ^= 1;
+    }
+  };
+  TileWalk tile(blockIdx.x, gridDim.x, p.hq, p.S);
   if (warp == 0) {
-    bool ok = true;
-    int it = 0, jj = 0;
-    TileWalk tile(blockIdx.x, gridDim.x, p.hq, p.S);
+    int entry = 0;
     for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it, tile.next()) {
       const Blocks<kKB> kb(tile.q0, p.S, p.window, p.sinks);
       const int kvh = tile.h / grp;
       if (it > 0 && !(ok = warp_wait(a_full, (it - 1) & 1))) break;  // the last tile's have been copied
       if (elect_one()) {
-        mbar_arrive_expect_tx(q_full, 3 * C::TILE);
+        mbar_arrive_expect_tx(q_full, 2 * C::TILE);
         load_tile<HD>(sQ, C::CH, &tmQ, q_full, tile.h * HD, tile.q0, tile.b);
         load_tile<HD>(sO, C::CH, &tmO, q_full, tile.h * HD, tile.q0, tile.b);
-        load_tile<HD>(sF, C::CH, &tmFo, q_full, tile.h * HD, tile.q0, tile.b);
       }
       __syncwarp();
-      for (int j = 0; j < kb.n && ok; ++j, ++jj) {
-        const int k0 = kb.k0(j), w = kb.width(j), s = jj & 1;
-        if (jj >= 2 && !(ok = warp_wait(k_empty + s, ((jj >> 1) - 1) & 1))) break;
-        if (elect_one()) load_keys<HD, kKB>(sK + s * C::TILE, C::CH, &tmK, &tmK16, k_full + s, kvh * HD, k0, w, tile.b);
+      for (int j = -1; j < kb.n; ++j, ++entry, advance(1)) {  // -1: o
+        if (entry >= C::NK && !(ok = warp_wait(k_empty + slot, par ^ 1))) break;
+        if (elect_one()) {
+          if (j < 0) {
+            mbar_arrive_expect_tx(k_full + slot, C::TILE);
+            load_tile<HD>(sK + slot * C::TILE, C::CH, &tmFo, k_full + slot, tile.h * HD, tile.q0, tile.b);
+          } else {
+            load_keys<HD, kKB>(sK + slot * C::TILE, C::CH, &tmK, &tmK16, k_full + slot, kvh * HD, kb.k0(j), kb.width(j), tile.b);
+          }
+        }
         __syncwarp();
+        if (j < 0) continue;
         if (jj >= 1 && !(ok = warp_wait(v_empty, (jj - 1) & 1))) break;
-        if (elect_one()) load_keys<HD, kKB>(sV, C::CH, &tmV, &tmV16, v_full, kvh * HD, k0, w, tile.b);
+        if (elect_one()) load_keys<HD, kKB>(sV, C::CH, &tmV, &tmV16, v_full, kvh * HD, kb.k0(j), kb.width(j), tile.b);
         __syncwarp();
+        ++jj;
       }
     }
   } else if (warp == 1) {
     constexpr uint32_t idQ = umma_idesc_bf16(128, HD, 0, 1);
-    bool ok = true;
-    const auto scores = [&](int jj, int w) {  // S = Q K^T
-      if (!(ok = ok && warp_wait(k_full + (jj & 1), (jj >> 1) & 1))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_tt<HD>(tS, tA, make_desc(smem_u32(sK + (jj & 1) * C::TILE), 16, 1024), C::CH, umma_idesc_bf16(128, w, 0, 0));
-        umma_commit(s_full);
-      }
-      __syncwarp();
+    const Desc kk = make_desc(smem_u32(sK), 16, 1024), km = make_desc(smem_u32(sK), C::CH, 1024);  // K- and MN-major
+    const Desc vk = make_desc(smem_u32(sV), 16, 1024);
+    const auto scores = [&](int w) {  // S = Q K^T
+      mma_tt<HD>(tS, tA, at(kk, slot * C::TILE), C::CH, umma_idesc_bf16(128, w, 0, 0));
+      umma_commit(s_full);
     };
-    const auto dprobs = [&](int jj, int w) {  // dP = dO V^T
-      if (!(ok = ok && warp_wait(v_full, jj & 1))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_tt<HD>(tP, tA + 64, make_desc(smem_u32(sV), 16, 1024), C::CH, umma_idesc_bf16(128, w, 0, 0));
-        umma_commit(dp_full);
-        umma_commit(v_empty);
-      }
-      __syncwarp();
+    const auto dprobs = [&](int w) {  // dP = dO V^T
+      mma_tt<HD>(tP, tA + 64, vk, C::CH, umma_idesc_bf16(128, w, 0, 0));
+      umma_commit(dp_full);
+      umma_commit(v_empty);
     };
-    int it = 0, jj = 0;
-    TileWalk tile(blockIdx.x, gridDim.x, p.hq, p.S);
     for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it, tile.next()) {
       const Blocks<kKB> kb(tile.q0, p.S, p.window, p.sinks);
-      if (!(ok = warp_wait(a_full, it & 1))) break;
-      scores(jj, kb.width(0));
-      dprobs(jj, kb.width(0));
-      for (int j = 0; j < kb.n && ok; ++j, ++jj) {
-        const int next = j + 1 < kb.n ? kb.width(j + 1) : 0;
-        if (next) {
-          if (!(ok = warp_wait(s_free, jj & 1))) break;
-          scores(jj + 1, next);
+      advance(1);
+      if (!(ok = warp_wait(a_full, it & 1) && warp_wait(k_full + slot, par))) break;
+      tc_fence_after();
+      int w = kb.width(0);
+      if (elect_one()) scores(w);
+      __syncwarp();
+      if (!(ok = warp_wait(v_full, jj & 1))) break;
+      tc_fence_after();
+      if (elect_one()) dprobs(w);
+      __syncwarp();
+      for (int j = 0; j < kb.n; ++j, ++jj) {
+        const bool more = j + 1 < kb.n;
+        const int next = more ? kb.width(j + 1) : 0, cur = slot;
+        advance(1);
+        if (more) {
+          if (!(ok = warp_wait2(s_free, jj & 1, k_full + slot, par))) break;
+          tc_fence_after();
+          if (elect_one()) scores(next);
+          __syncwarp();
         }
         // dS is written; with a tile's first block its threads have also read the last tile's dQ
-        if (!(ok = ok && warp_wait(ds_full, jj & 1))) break;
+        if (!(ok = more ? warp_wait2(v_full, (jj + 1) & 1, ds_full, jj & 1) : warp_wait(ds_full, jj & 1))) break;
         tc_fence_after();
         if (elect_one()) {  // each half of a block's columns holds its own 64 keys' dS
-          mma_ts<kKB, 64>(tQ, tP, make_desc(smem_u32(sK + (jj & 1) * C::TILE), C::CH, 1024), idQ, kb.width(j), j > 0);
-          umma_commit(k_empty + (jj & 1));
-          if (!next) umma_commit(done);
+          mma_ts<kKB, 64>(tQ, tP, at(km, cur * C::TILE), idQ, w, j > 0);
+          umma_commit(k_empty + cur);
+          if (more) dprobs(next);
+          else umma_commit(done);
         }
         __syncwarp();
-        if (next) dprobs(jj + 1, next);
+        w = next;
       }
     }
   } else {
@@ -753,57 +771,57 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     const uint32_t tX = tS + g * 64 + lanes, tY = tP + g * 64 + lanes;
     const float sl2 = p.scale * kLog2e;
     const uint64_t sl = f2(sl2, sl2);
-    bool ok = true;
-    TileWalk tile(blockIdx.x, gridDim.x, p.hq, p.S);
     const auto load_lse = [&] {
       return tile.q0 + r < p.S ? p.lse[((int64_t)tile.b * p.S + tile.q0 + r) * p.hq + tile.h] : INFINITY;
     };
-    float lse = load_lse();  // fetched under the tile in front
-    int it = 0, jj = 0;
-    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it) {
-      const int q0 = tile.q0, h = tile.h, b = tile.b, i = q0 + r;
-      const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
-      // a wait that runs out is shared at the next barrier, which every warp reaches
-      ok = warp_wait(q_full, it & 1);
-      {  // the first four warps copy Q's rows into TMEM, the others dO's, forming D = dO . o as well
-        const uint8_t* src = g ? sO : sQ;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    // the first four warps copy Q's rows of tile `n` into TMEM, the others dO's, forming D = dO . o as well
+    const auto copy = [&](int n) {
+      if (!warp_wait(q_full, n & 1) || (g == 1 && !warp_wait(k_full + slot, par))) return false;
+      const uint8_t *src = g ? sO : sQ, *so = sK + slot * C::TILE;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < HD / 64; ++c) {
-          uint32_t w[32];
+      for (int c = 0; c < HD / 64; ++c) {
+        uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(w + 4 * e) = *reinterpret_cast<const uint4*>(src + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
-          tmem_st32(tA + g * 64 + c * 32 + lanes, w);
-          if (g == 1) {
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(w + 4 * e) = *reinterpret_cast<const uint4*>(src + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
+        tmem_st32(tA + g * 64 + c * 32 + lanes, w);
+        if (g == 1) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint4 o4 = *reinterpret_cast<const uint4*>(sF + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
-              const uint32_t o[4] = {o4.x, o4.y, o4.z, o4.w};
+          for (int e = 0; e < 8; ++e) {
+            const uint4 o4 = *reinterpret_cast<const uint4*>(so + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
+            const uint32_t o[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const float2 d2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(w + 4 * e + u));
-                const float2 o2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(o + u));
-                sum[u] = fmaf(d2.x, o2.x, fmaf(d2.y, o2.y, sum[u]));
-              }
+            for (int u = 0; u < 4; ++u) {
+              const float2 d2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(w + 4 * e + u));
+              const float2 o2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(o + u));
+              sum[u] = fmaf(d2.x, o2.x, fmaf(d2.y, o2.y, sum[u]));
             }
           }
         }
-        if (g == 1) sD[r] = i < p.S ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(a_full);
       }
-      if (warp == 2) tma_store_wait();  // the last tile's dQ has left sG
-      if (!(ok = sync_all(1, 256, ok))) break;
-      const float D = sD[r], lse2 = lse * kLog2e;
+      if (g == 1) sD[(n & 1) * kQB + r] = tile.q0 + r < p.S ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(a_full);
+      return true;
+    };
+    float lse = load_lse();
+    // a wait that runs out is shared at the next barrier, which every warp reaches
+    ok = sync_all(1, 256, copy(0));
+    if (ok && warp == 2 && elect_one()) mbar_arrive(k_empty + slot);
+    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it) {
+      const int q0 = tile.q0, h = tile.h, b = tile.b, i = q0 + r;
+      const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
+      const bool another = x + gridDim.x < tiles;
+      const float D = sD[(it & 1) * kQB + r], lse2 = lse * kLog2e;
       const uint64_t ln = f2(-lse2, -lse2), Dn = f2(-D, -D);
       p.D[stat_row(b, h, p.hq, p.S) + g * up(p.S, kQB) + i] = g ? D : lse2;
-      if (x + gridDim.x < tiles) {
+      if (another) {
         tile.next();
-        lse = load_lse();
+        lse = load_lse();  // under this tile
       }
-      for (int j = 0; j < kb.n && ok; ++j, ++jj) {  // columns [64 g, 64 g + 64) of each block
+      for (int j = 0; j < kb.n; ++j, ++jj) {  // columns [64 g, 64 g + 64) of each block
         if (!(ok = warp_wait(s_full, jj & 1))) break;
         tc_fence_after();
         const int k0 = kb.k0(j);
@@ -834,8 +852,11 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         tmem_st16(tY + 16, w + 16);
         tmem_st_wait();
         tc_fence_before();
+        if (warp == 2 && j + 1 == kb.n) tma_store_wait();  // the last tile's dQ has left sG; `done` tells the others
         mbar_arrive(ds_full);
       }
+      advance(kb.n + 1);  // o of the next tile
+      if (ok && another) ok = copy(it + 1);
       if ((ok = ok && warp_wait(done, it & 1))) {
         tc_fence_after();
         float lo[HD / 4], hi[HD / 4];
@@ -846,6 +867,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       }
       if (!(ok = sync_all(1, 256, ok))) break;
       if (warp == 2 && elect_one()) {
+        if (another) mbar_arrive(k_empty + slot);
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c) tma_store_3d(&tmDq, sG + c * C::CH, h * HD + c * 64, q0, b);
       }
@@ -1033,49 +1055,56 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     const Desc dK = make_desc(smem_u32(sK), 16, 1024), dV = make_desc(smem_u32(sV), 16, 1024);
     const Desc qk = make_desc(smem_u32(sQ), 16, 1024), qm = make_desc(smem_u32(sQ), C::CH, 1024);  // K- and MN-major
     const Desc ok_ = make_desc(smem_u32(sO), 16, 1024), om = make_desc(smem_u32(sO), C::CH, 1024);
-    // slots of the rings of Q and dO and the parities of their phases: of this item and, for Q, of the next
+    // the next slots of the rings of Q and dO and the parities of their phases
     int sq = 0, so = 0;
     uint32_t pq = 0, po = 0;
     const auto scores = [&] {  // S^T = K Q^T
       mma_ss<HD>(tS, dK, C::CH, at(qk, sq * C::TILE), C::CH, idS);
       umma_commit(s_full);
     };
+    const auto dprobs = [&] {  // dP^T = V dO^T
+      mma_ss<HD>(tP, dV, C::CH, at(ok_, so * C::TILE), C::CH, idS);
+      umma_commit(dp_full);
+    };
     for (int seg = 0; ok && my.next(sp); ++seg) {
-      if (!(ok = warp_wait(kv_full, seg & 1) && warp_wait(&q_full[sq], pq))) break;
+      if (!(ok = warp_wait2(kv_full, seg & 1, &q_full[sq], pq))) break;
       tc_fence_after();
       if (elect_one()) scores();
       __syncwarp();
+      if (!(ok = warp_wait(&o_full[so], po))) break;
+      tc_fence_after();
+      if (elect_one()) dprobs();
+      __syncwarp();
       bool add = false;
       for (int n = my.i1 - my.i0; n > 0; --n, ++jj) {
-        const int q0 = sq;
+        const int q0 = sq, o0 = so;
         if (++sq == C::NQ) {
           sq = 0;
           pq ^= 1;
         }
-        if (!(ok = n > 1 ? warp_wait3(&o_full[so], po, s_free, jj & 1, &q_full[sq], pq) : warp_wait(&o_full[so], po))) break;
-        tc_fence_after();
-        if (elect_one()) {  // dP^T = V dO^T, and the next item's scores
-          mma_ss<HD>(tP, dV, C::CH, at(ok_, so * C::TILE), C::CH, idS);
-          umma_commit(dp_full);
-          if (n > 1) scores();
-        }
-        __syncwarp();
-        // dS and P are written; with a tile's first item its threads have also read the last tile's dV and dK
-        if (!(ok = warp_wait(ds_full, jj & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          mma_ts<C::QB, 32>(tV, tP + 16, at(om, so * C::TILE), idG, C::QB, add);
-          umma_commit(&o_empty[so]);
-          mma_ts<C::QB, 32>(tK, tP, at(qm, q0 * C::TILE), idG, C::QB, add);
-          umma_commit(&q_empty[q0]);
-          if (n == 1) umma_commit(done);
-        }
-        __syncwarp();
-        add = true;
         if (++so == C::NO) {
           so = 0;
           po ^= 1;
         }
+        if (n > 1) {
+          if (!(ok = warp_wait2(s_free, jj & 1, &q_full[sq], pq))) break;
+          tc_fence_after();
+          if (elect_one()) scores();
+          __syncwarp();
+        }
+        // dS and P are written; with a tile's first item its threads have also read the last tile's dV and dK
+        if (!(ok = n > 1 ? warp_wait2(&o_full[so], po, ds_full, jj & 1) : warp_wait(ds_full, jj & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_ts<C::QB, 32>(tV, tP + 16, at(om, o0 * C::TILE), idG, C::QB, add);
+          umma_commit(&o_empty[o0]);
+          mma_ts<C::QB, 32>(tK, tP, at(qm, q0 * C::TILE), idG, C::QB, add);
+          umma_commit(&q_empty[q0]);
+          if (n > 1) dprobs();
+          else umma_commit(done);
+        }
+        __syncwarp();
+        add = true;
       }
     }
   } else {
