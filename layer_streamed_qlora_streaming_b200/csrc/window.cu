@@ -623,7 +623,7 @@ struct DqCfg {
   static constexpr int KB = 128, NK = 3;  // keys of a block, blocks of K in flight
   static constexpr uint32_t CH = kQB * 128;
   static constexpr uint32_t TILE = (HD / 64) * CH;
-  static constexpr uint32_t SMEM = 7 * TILE + 1024 + 256 + 2 * kQB * 4;
+  static constexpr uint32_t SMEM = 7 * TILE + 256 + 4 * kQB * 4;
 };
 
 template <int HD>
@@ -635,17 +635,20 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
             const int tiles) {
   using C = DqCfg<HD>;
   constexpr int kKB = C::KB;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];  // no room to round up: its start is aligned
+  if (smem_u32(smem_tiles) & 1023) {  // for every thread alike
+    dev_fail(DEV_ERR_BAD_INDEX);
+    return;
+  }
   // Q, dO, K and o [NK], V, dQ on its way out
-  uint8_t *sQ = smem, *sO = sQ + C::TILE, *sK = sO + C::TILE, *sV = sK + C::NK * C::TILE, *sG = sV + C::TILE;
+  uint8_t *sQ = smem_tiles, *sO = sQ + C::TILE, *sK = sO + C::TILE, *sV = sK + C::NK * C::TILE, *sG = sV + C::TILE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sG + C::TILE);
   uint64_t *a_full = bars, *s_free = bars + 1, *ds_full = bars + 2;  // of all 256 row threads
   uint64_t *q_full = bars + 3, *s_full = bars + 4, *dp_full = bars + 5, *done = bars + 6, *v_full = bars + 7,
            *v_empty = bars + 8, *k_full = bars + 9, *k_empty = k_full + C::NK;
   constexpr int kBars = 9 + 2 * C::NK;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
-  float* sD = reinterpret_cast<float*>(bars + kBars + 1);  // [2][128], by tile
+  float* sD = reinterpret_cast<float*>(bars + kBars + 1);  // [2][2][128]: of a tile, the halves of D
   const int grp = p.hq / p.hkv;
   const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -774,33 +777,33 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     const auto load_lse = [&] {
       return tile.q0 + r < p.S ? p.lse[((int64_t)tile.b * p.S + tile.q0 + r) * p.hq + tile.h] : INFINITY;
     };
-    // the first four warps copy Q's rows of tile `n` into TMEM, the others dO's, forming D = dO . o as well
+    // the first four warps copy Q's rows of tile `n` into TMEM, the others dO's; each of them forms D = dO . o over
+    // half of the columns
     const auto copy = [&](int n) {
-      if (!warp_wait(q_full, n & 1) || (g == 1 && !warp_wait(k_full + slot, par))) return false;
-      const uint8_t *src = g ? sO : sQ, *so = sK + slot * C::TILE;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      if (!warp_wait2(q_full, n & 1, k_full + slot, par)) return false;
+      const auto row = [&](const uint8_t* t, int e) {  // columns [8 e, 8 e + 8)
+        return reinterpret_cast<const uint4*>(t + e / 8 * C::CH + r * 128 + ((e % 8) ^ (r & 7)) * 16);
+      };
 #pragma unroll
       for (int c = 0; c < HD / 64; ++c) {
         uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(w + 4 * e) = *reinterpret_cast<const uint4*>(src + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
+        for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(w + 4 * e) = *row(g ? sO : sQ, 8 * c + e);
         tmem_st32(tA + g * 64 + c * 32 + lanes, w);
-        if (g == 1) {
+      }
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint4 o4 = *reinterpret_cast<const uint4*>(so + c * C::CH + r * 128 + ((e ^ (r & 7)) * 16));
-            const uint32_t o[4] = {o4.x, o4.y, o4.z, o4.w};
+      for (int e = 0; e < HD / 16; ++e) {
+        const uint4 d4 = *row(sO, g * (HD / 16) + e), o4 = *row(sK + slot * C::TILE, g * (HD / 16) + e);
+        const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w}, o[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float2 d2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(w + 4 * e + u));
-              const float2 o2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(o + u));
-              sum[u] = fmaf(d2.x, o2.x, fmaf(d2.y, o2.y, sum[u]));
-            }
-          }
+        for (int u = 0; u < 4; ++u) {
+          const float2 d2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(d + u));
+          const float2 o2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(o + u));
+          sum[u] = fmaf(d2.x, o2.x, fmaf(d2.y, o2.y, sum[u]));
         }
       }
-      if (g == 1) sD[(n & 1) * kQB + r] = tile.q0 + r < p.S ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+      sD[((n & 1) * 2 + g) * kQB + r] = tile.q0 + r < p.S ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(a_full);
@@ -814,7 +817,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       const int q0 = tile.q0, h = tile.h, b = tile.b, i = q0 + r;
       const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
       const bool another = x + gridDim.x < tiles;
-      const float D = sD[(it & 1) * kQB + r], lse2 = lse * kLog2e;
+      const float D = sD[(it & 1) * 2 * kQB + r] + sD[((it & 1) * 2 + 1) * kQB + r], lse2 = lse * kLog2e;
       const uint64_t ln = f2(-lse2, -lse2), Dn = f2(-D, -D);
       p.D[stat_row(b, h, p.hq, p.S) + g * up(p.S, kQB) + i] = g ? D : lse2;
       if (another) {
