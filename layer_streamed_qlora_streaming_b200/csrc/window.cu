@@ -314,37 +314,30 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc bb, uint32_t
 }
 
 // ---------------------------------------------------------------------------------- forward
-// The query tile of CTA x: heads of a tile next to each other, the last tiles (the longest) first.
+// Query tile x of the tiles of `heads` heads (of all sequences): the sequences' last tiles (the longest) first, heads of a tile next to each other.
 struct QueryTile {
   int h, b, q0;
-  __device__ __forceinline__ QueryTile(int x, int hq, int S) {
-    const int nq = (S + kQB - 1) / kQB, u = x / hq;
-    h = x % hq;
-    b = u / nq;
-    q0 = (nq - 1 - u % nq) * kQB;
+  __device__ __forceinline__ QueryTile(int x, int hq, int heads, int S) {
+    const int q = x / heads, u = x - q * heads;
+    b = u / hq;
+    h = u - b * hq;
+    q0 = ((S + kQB - 1) / kQB - 1 - q) * kQB;
   }
 };
-
-// The same for a CTA that takes every step-th tile, without a division a tile.
+// The tiles of CTA c of n in its order: c, 2 n - 1 - c, 2 n + c, ...: back and forth, so that no CTA gets the longer tile
+// in every round. (Of 4 sequences of 512 tokens the longest CTA then has 3 or 4 tiles of mixed lengths, 35500 clocks
+// by their blocks instead of 44100 with each n-th tile by sequence.)
 struct TileWalk : QueryTile {
-  int nq, hq, dh, dq, db;
-  __device__ __forceinline__ TileWalk(int x, int step, int hq_, int S) : QueryTile(x, hq_, S) {
-    hq = hq_;
-    nq = (S + kQB - 1) / kQB;
-    dh = step % hq;
-    dq = step / hq % nq;
-    db = step / hq / nq;
+  int x, round;
+  __device__ __forceinline__ TileWalk(int hq, int heads, int S) : QueryTile(blockIdx.x, hq, heads, S), x(blockIdx.x), round(0) {}
+  __device__ __forceinline__ int after() const {
+    const int n = gridDim.x, c = blockIdx.x;
+    return (round + 1) * n + (round & 1 ? c : n - 1 - c);
   }
-  __device__ __forceinline__ void next() {
-    h += dh;
-    const int carry = h >= hq;
-    if (carry) h -= hq;
-    q0 -= (dq + carry) * kQB;
-    b += db;
-    if (q0 < 0) {
-      q0 += nq * kQB;
-      ++b;
-    }
+  __device__ __forceinline__ void next(int hq, int heads, int S) {
+    x = after();
+    ++round;
+    static_cast<QueryTile&>(*this) = QueryTile(x, hq, heads, S);
   }
 };
 
@@ -379,7 +372,7 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
            *v_empty = bars + 8, *s_full = bars + 10, *p_full = bars + 12;  // [2] from k_full on
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
 
-  const QueryTile tile(blockIdx.x, p.hq, p.S);
+  const QueryTile tile(blockIdx.x, p.hq, p.heads, p.S);
   const int h = tile.h, b = tile.b, q0 = tile.q0;
   const int kvh = h / (p.hq / p.hkv);
   const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
@@ -415,7 +408,7 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     bool ok = true;
     for (int j = 0; j < kb.n && ok; ++j) {
       if (j == 2 && blockIdx.x + ahead < gridDim.x && elect_one()) {
-        const QueryTile next(blockIdx.x + ahead, p.hq, p.S);
+        const QueryTile next(blockIdx.x + ahead, p.hq, p.heads, p.S);
         prefetch_tile<HD>(&tmQ, next.h * HD, next.q0, next.b);
       }
       const int k0 = kb.k0(j), w = kb.width(j), s = j & 1;
@@ -688,10 +681,10 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       par ^= 1;
     }
   };
-  TileWalk tile(blockIdx.x, gridDim.x, p.hq, p.S);
+  TileWalk tile(p.hq, p.heads, p.S);
   if (warp == 0) {
     int entry = 0;
-    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it, tile.next()) {
+    for (; tile.x < tiles && ok; ++it, tile.next(p.hq, p.heads, p.S)) {
       const Blocks<kKB> kb(tile.q0, p.S, p.window, p.sinks);
       const int kvh = tile.h / grp;
       if (it > 0 && !(ok = warp_wait(a_full, (it - 1) & 1))) break;  // the last tile's have been copied
@@ -732,7 +725,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       umma_commit(dp_full);
       umma_commit(v_empty);
     };
-    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it, tile.next()) {
+    for (; tile.x < tiles && ok; ++it, tile.next(p.hq, p.heads, p.S)) {
       const Blocks<kKB> kb(tile.q0, p.S, p.window, p.sinks);
       advance(1);
       if (!(ok = warp_wait(a_full, it & 1) && warp_wait(k_full + slot, par))) break;
@@ -813,15 +806,15 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
     // a wait that runs out is shared at the next barrier, which every warp reaches
     ok = sync_all(1, 256, copy(0));
     if (ok && warp == 2 && elect_one()) mbar_arrive(k_empty + slot);
-    for (int x = blockIdx.x; x < tiles && ok; x += gridDim.x, ++it) {
+    for (bool another = true; another && ok; ++it) {
       const int q0 = tile.q0, h = tile.h, b = tile.b, i = q0 + r;
       const Blocks<kKB> kb(q0, p.S, p.window, p.sinks);
-      const bool another = x + gridDim.x < tiles;
+      another = tile.after() < tiles;
       const float D = sD[(it & 1) * 2 * kQB + r] + sD[((it & 1) * 2 + 1) * kQB + r], lse2 = lse * kLog2e;
       const uint64_t ln = f2(-lse2, -lse2), Dn = f2(-D, -D);
       p.D[stat_row(b, h, p.hq, p.S) + g * up(p.S, kQB) + i] = g ? D : lse2;
       if (another) {
-        tile.next();
+        tile.next(p.hq, p.heads, p.S);
         lse = load_lse();  // under this tile
       }
       for (int j = 0; j < kb.n; ++j, ++jj) {  // columns [64 g, 64 g + 64) of each block
@@ -1422,6 +1415,7 @@ cudaError_t window_fwd(WinArgs a, cudaStream_t s) {
   if (!window_shape_ok(a.T, a.S, a.hq, a.hkv, a.hd, a.window, a.sinks)) return cudaErrorInvalidValue;
   a.window = std::min(a.window, a.S);
   a.sinks = std::min(a.sinks, a.S);
+  a.heads = (int)(a.T / a.S) * a.hq;
   const cudaError_t e = a.hd == 128 ? launch_fwd<128>(a, s) : launch_fwd<64>(a, s);
   note_launch(1);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -1431,6 +1425,7 @@ cudaError_t window_bwd(WinBwdArgs a, cudaStream_t s) {
   if (!window_shape_ok(a.T, a.S, a.hq, a.hkv, a.hd, a.window, a.sinks)) return cudaErrorInvalidValue;
   a.window = std::min(a.window, a.S);
   a.sinks = std::min(a.sinks, a.S);
+  a.heads = (int)(a.T / a.S) * a.hq;
   const cudaError_t e = a.hd == 128 ? launch_bwd<128>(a, s) : launch_bwd<64>(a, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

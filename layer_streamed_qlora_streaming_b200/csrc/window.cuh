@@ -9,10 +9,12 @@ namespace lst {
 struct WinArgs : AttnArgs {
   int window;  // >= 1
   int sinks;   // >= 0
+  int heads;   // T / S * hq, set by window_fwd (window_bwd)
 };
 struct WinBwdArgs : AttnBwdArgs {  // D: window_scratch() floats, 16-byte aligned
   int window;
   int sinks;
+  int heads;
 };
 
 bool window_shape_ok(int64_t T, int S, int hq, int hkv, int hd, int window, int sinks);
