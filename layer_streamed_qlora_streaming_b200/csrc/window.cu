@@ -57,36 +57,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// 2^x of a pair on the FMA pipe: x = n + f with n the nearest whole number (by adding 1.5 * 2^23, whose low
-// bits then hold n), 2^f on [-1/2, 1/2] by the polynomial of degree 4 of least relative error (2.7e-6, by
-// Remez' exchange), n added to its exponent. For x up to 120; 0 below -125 and for -infinity. The
-// exponential unit gives 16 values a clock and SM, 1024 clocks for a tile of 128 x 128, and in the backward
-// kernels the threads' chain is what a block takes: of the backward of 8192 tokens none of the pairs on the
-// FMA pipe take 532 us, a quarter 524, half 513, three quarters 531. (The forward, with two CTAs an SM,
-// is not bound by it: 289 us with none, 295 with a quarter.)
+// 2^x of a pair. (Every other pair by a polynomial on the FMA pipe, to spare the exponential unit, made the backward
+// of 8192 tokens 2 % longer and that of 4 x 512 tokens 1.5 % shorter.)
 __device__ __forceinline__ void ex2_pair(uint64_t x, float& r0, float& r1) {
-  constexpr float kMagic = 12582912.f;
-  const uint64_t t = add2(x, f2(kMagic, kMagic)), f = fma2(add2(t, f2(-kMagic, -kMagic)), f2(-1.f, -1.f), x);
-  uint64_t q = fma2(f, f2(0.009570102f, 0.009570102f), f2(0.05591786f, 0.05591786f));
-  q = fma2(q, f, f2(0.24024744f, 0.24024744f));
-  q = fma2(q, f, f2(0.6931218f, 0.6931218f));
-  q = fma2(q, f, f2(0.9999993f, 0.9999993f));
-  float x0, x1, t0, t1, q0, q1;
-  unpack(x, x0, x1);
-  unpack(t, t0, t1);
-  unpack(q, q0, q1);
-  r0 = x0 < -125.f ? 0.f : __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
-  r1 = x1 < -125.f ? 0.f : __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
-}
-// 2^x of pair n of a run, every other one by ex2_pair
-__device__ __forceinline__ void ex2_of(int n, uint64_t x, float& r0, float& r1) {
-  if (n % 2 == 0) {
-    ex2_pair(x, r0, r1);
-  } else {
-    unpack(x, r0, r1);
-    r0 = ex2_approx(r0);
-    r1 = ex2_approx(r1);
-  }
+  unpack(x, r0, r1);
+  r0 = ex2_approx(r0);
+  r1 = ex2_approx(r1);
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -503,9 +479,7 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 #pragma unroll
       for (int c = 0; c < kKB / 2; ++c) {
         float a0, a1;
-        unpack(fma2(f2(x[2 * c], x[2 * c + 1]), sl, mn), a0, a1);
-        a0 = ex2_approx(a0);
-        a1 = ex2_approx(a1);
+        ex2_pair(fma2(f2(x[2 * c], x[2 * c + 1]), sl, mn), a0, a1);
         ps[c & 1] = add2(ps[c & 1], f2(a0, a1));
         w[c] = pack2(a0, a1);
       }
@@ -827,7 +801,7 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         tc_fence_before();
         mbar_arrive(s_free);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) ex2_of(c, fma2(f2(a[2 * c], a[2 * c + 1]), sl, ln), a[2 * c], a[2 * c + 1]);
+        for (int c = 0; c < 32; ++c) ex2_pair(fma2(f2(a[2 * c], a[2 * c + 1]), sl, ln), a[2 * c], a[2 * c + 1]);
         if (!all_visible(q0, kQB, k0, kKB, p.window, p.sinks)) {  // also what lies behind a narrower block
           const uint64_t vis = visible_keys(i, k0 + g * 64, p.window, p.sinks);
           const uint32_t bits[2] = {(uint32_t)vis, (uint32_t)(vis >> 32)};
@@ -1126,8 +1100,8 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
         for (int c = 0; c < 64; c += 4) {
           const float4 l4 = lse[c / 4];
-          ex2_of(c / 2, fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
-          ex2_of(c / 2 + 1, fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
+          ex2_pair(fma2(f2(x[c], x[c + 1]), sl, f2(-l4.x, -l4.y)), x[c], x[c + 1]);
+          ex2_pair(fma2(f2(x[c + 2], x[c + 3]), sl, f2(-l4.z, -l4.w)), x[c + 2], x[c + 3]);
         }
         if (!all_visible(q, C::QB, k0, kQB, p.window, p.sinks)) {
           const uint64_t vis = visible_queries(key, q + half * 64, p.window, p.sinks);
