@@ -199,7 +199,10 @@ constexpr int kZeroBytes = 1024;
 //    (st.async of each CTA's pair into its peers, onto their mbarrier), in a fixed order; the row's
 //    factor coef 2^((m - lse) log2 e) then turns e into dlogits with one product.
 // Each logit crosses HBM once and takes one exponential. Bound by HBM: 4 + 2 bytes a logit, 2 bytes on
-// rows that do not count.
+// rows that do not count. 4096 rows of 151936 logits, most of them counted, take 467 us, 0.90 of the rate of a plain
+// copy; 2048 rows of 128256, half of them counted, 212 us, 0.76: clusters of 8 fill 264 of 296 places, and reads
+// and the uncounted rows' writes alternate; 999 rows of 32003, 28 us, 0.51: a row's chain of load, exchange
+// and stores comes three or four times for each CTA. (A CTA a row, read twice: 3896, 1461 and 75 us.)
 template <int NV, int THREADS, int PER_SM>
 __global__ void __launch_bounds__(THREADS, PER_SM)
 k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int early) {

@@ -7,8 +7,8 @@
 // the last two over the query heads h that share the kv head.
 //
 // Three kernels on tcgen05 (bf16 operands, fp32 in TMEM), each walking only the tiles that hold a
-// visible pair: the forward, dQ (which forms D first), and dK / dV, whose sums over heads and queries
-// are split over CTAs where there would be too few, or, for the keys that are sinks, too long ones.
+// visible pair: the forward, dQ (which forms D first), and dK / dV, whose work is cut into equal shares; a
+// fourth adds the parts of what was cut.
 // Tiles come by 3D TMA maps (column, row of the sequence, sequence): rows behind a sequence read as
 // zeros, never as the next sequence. P and dS are rounded to bf16 as operands (half a step of 2^-8
 // relative, independent of the output's own rounding); everything else is fp32.
@@ -274,7 +274,7 @@ __device__ __forceinline__ void mma_ss(uint32_t d, Desc a, uint32_t achunk, Desc
     umma_ss(d, at(a, (kk >> 2) * achunk + (kk & 3) * 32), at(bb, (kk >> 2) * bchunk + (kk & 3) * 32), id, kk != 0);
 }
 // D (+)= A B over w <= N rows of B (MN-major, 128-byte rows): A bf16 in TMEM, 16 rows of B every 8 columns; with HALF,
-// rows [HALF, ...) of it HALF columns behind the first
+// each HALF rows HALF columns behind the last ones
 template <int N, int HALF>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc bb, uint32_t id, int w, bool add) {
   const auto step = [&](int kk, uint32_t acc) {
@@ -290,7 +290,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc bb, uint32_t
 }
 
 // ---------------------------------------------------------------------------------- forward
-// Query tile x of the tiles of `heads` heads (of all sequences): the sequences' last tiles (the longest) first, heads of a tile next to each other.
+// Query tile x of those of `heads` heads (of all sequences): the sequences' last tiles (the longest) first, the heads
+// of a tile next to each other.
 struct QueryTile {
   int h, b, q0;
   __device__ __forceinline__ QueryTile(int x, int hq, int heads, int S) {
@@ -301,8 +302,8 @@ struct QueryTile {
   }
 };
 // The tiles of CTA c of n in its order: c, 2 n - 1 - c, 2 n + c, ...: back and forth, so that no CTA gets the longer tile
-// in every round. (Of 4 sequences of 512 tokens the longest CTA then has 3 or 4 tiles of mixed lengths, 35500 clocks
-// by their blocks instead of 44100 with each n-th tile by sequence.)
+// in every round. (The backward of 4 sequences of 512 tokens takes 57.4 us so, 60.4 with every n-th tile of the
+// sequences one behind the other.)
 struct TileWalk : QueryTile {
   int x, round;
   __device__ __forceinline__ TileWalk(int hq, int heads, int S) : QueryTile(blockIdx.x, hq, heads, S), x(blockIdx.x), round(0) {}
@@ -324,6 +325,11 @@ struct TileWalk : QueryTile {
 // While a row's thread works on block j, the tensor cores form P V of j - 1 and S of j + 1.
 // The reference m of a row moves only when a block's maximum exceeds it by 2^8; O is then rescaled in
 // TMEM, once P V of j - 1 has been added. The tile of O leaves through Q's shared memory by TMA.
+// Bound by the hand-over between MMAs and row threads: 16384 tokens, 32 heads of 128 over 8, window 1024, 4 sinks
+// take 288 us, 0.55 of the matrix rate that a large product reaches, the tensor pipe 50 % active (an S of N = 64
+// takes 48 clocks an MMA where 32 would do: both operands come from shared memory); 4 x 512 tokens 17.7 us, 20 %
+// active: 512 CTAs of 2 to 7 blocks, each with a start and an end. (Persistent CTAs with the next tile's Q and K
+// under this one's end took 292 us against 287, and 18.0 us against 18.4.)
 template <int HD>
 struct FwdCfg {
   static constexpr int KB = 64;  // keys of a block
@@ -580,11 +586,13 @@ __host__ __device__ __forceinline__ int64_t stat_row(int b, int h, int hq, int S
 // every block they took its whole bandwidth (128 bytes a clock: with K, V, their loads and dS K 1800
 // clocks a block, where the tensor cores take 1540), and their place is free for the next tile's. o, which
 // only D needs, passes through K's ring.
-// S of block j + 1 is issued right behind dP of j; dS goes over dP (bf16, the A operand of dQ += dS K), and dP of
-// j + 1 follows that product, under the exponentials of j + 1. (Blocks of 64 keys with two buffers of each
-// took 2060 clocks a block: at N = 64 the issue of an MMA takes longer than its 32 clocks.)
+// S of block j + 1 is issued once the threads have read S of j; dS goes over dP (bf16, the A operand of dQ += dS K),
+// and dP of j + 1 is issued in one run with that product, under the exponentials of j + 1. (Blocks of 64 keys with
+// two buffers of each took 2060 clocks for 64 keys: at N = 64 the issue of an MMA takes longer than its 32 clocks.)
 // A tile's end overlaps the next one's start: Q and dO of the next tile go to TMEM before dQ leaves it, so that
 // the first products run under dQ's way out (by TMA, from shared memory).
+// Bound by the chain dS -> dQ, dP -> dS of a block (about 2100 clocks, of which the tensor cores work 1540): 8192
+// tokens, 32 heads of 128 over 8, window 1024, 4 sinks take 204 us, the tensor pipe 55 % active; 4 x 512 tokens 28 us.
 template <int HD>
 struct DqCfg {
   static constexpr int KB = 128, NK = 3;  // keys of a block, blocks of K in flight
@@ -856,11 +864,11 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
 
 // ---------------------------------------------------------------------------------- dK, dV
 // An item is 128 keys of a kv head against 128 queries of one of its heads; the items of a key tile lie by head, by
-// query block. The tiles lie in a row, by sequence and kv head (a unit), those that hold sinks, whose
-// queries reach to the sequence's end, behind all others. Of its front each CTA takes every ctas-th tile whole, so that
-// the CTAs at work are on neighbouring tiles, which share most of Q and dO (with neighbouring tiles in one
-// CTA instead, 685 MB came from HBM for 9472 tokens rather than 196, and the kernel took 10 % longer);
-// the rest is cut, at fixed places, to make the CTAs' work equal. What a tile costs besides its items (K, V, the
+// query block. The tiles lie in a row, by sequence and kv head (a unit), those that hold sinks, whose queries
+// reach to the sequence's end, behind all others. Of the row's front each CTA takes every ctas-th tile whole, so
+// that the CTAs at work are on neighbouring tiles, which share most of Q and dO (with neighbouring tiles in one
+// CTA instead, 685 MB came from HBM for 9472 tokens rather than 196, and the kernel took 10 % longer); the rest
+// is cut, at fixed places, to make the CTAs' work equal. What a tile costs besides its items (K, V, the
 // stores) counts as kSeg items in front of them, which also moves cuts next to a tile's border onto the
 // border. The sums of a cut tile's parts go to the scratch as fp32, where k_window_join adds them in order.
 constexpr int kSms = 148, kSeg = 2;
@@ -870,7 +878,8 @@ struct Split {
   int grp;       // heads of a kv head
   int plain;     // tiles without sinks, of all units
   int ctas, rounds;  // each CTA's whole tiles
-  int tile[kSms + 1], off[kSms + 1];  // CTA c's share of the rest: from place off[c] of tile[c] to off[c + 1] of tile[c + 1]
+  // CTA c's share of the rest: from place off[c] of tile[c] to place off[c + 1] of tile[c + 1]
+  int tile[kSms + 1], off[kSms + 1];
   __host__ __device__ int blocks(int kb) const {  // query blocks that see a key tile
     const int n = nkb - kb;
     return kb < nsb || n < near ? n : near;
@@ -931,10 +940,15 @@ struct DkvCfg {
 //   S^T = K Q^T, P^T = 2^(S' - lse'), dP^T = V dO^T, dS^T = P^T (dP^T - D),
 //   dV += P^T dO, dK += dS^T Q with P^T and dS^T, as bf16 side by side over dP^T in TMEM, as A operands
 // (Q and dO read MN-major from the tiles used K-major for the scores). With dV, dK and both scores TMEM is
-// full; with K, V, three blocks of Q and two of dO shared memory is, too. P waits in registers for dP, so
-// that S of j + 1 is issued behind dP of j, and dV and dK of j, dP of j + 1 and S of j + 2 run under the
-// threads' work on j + 1. The products of an item are issued in two runs, since the tensor cores' queue is short: a
-// wait between each two of the four left them idle for 1000 clocks of the 3600 that an item then took.
+// full; with K, V, three blocks of Q and two of dO shared memory is, too. P waits in registers for dP, so that S
+// of j + 1 is issued once the threads have read S of j; dV and dK of j and dP of j + 1 are issued in one run, since
+// the tensor cores' queue is short and a wait in between leaves them idle.
+// (P over S makes the next S wait for dV: the backward of 8192 tokens took 518 us against 511. P in shared memory
+// leaves room for two blocks of Q only, whose loads then are the chain: 545 against 501. Blocks of 64 queries
+// with two buffers of each: 4000 clocks for 128 queries, as at N = 64 an MMA takes 48 clocks for 32.)
+// Bound by the chain dS -> dV, dK, dP -> dS (about 2900 clocks an item, of which the tensor cores work 2050): 8192
+// tokens, 32 heads of 128 over 8, window 1024, 4 sinks take 245 us, the tensor pipe 68 % active; 4 x 512 tokens
+// 34 us, the longest CTA 16 items, the mean 8.6.
 template <int HD>
 __global__ void __launch_bounds__(320, 1)
 k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
@@ -1190,7 +1204,8 @@ k_window_dkdv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 }
 
 // Adds the parts of a cut tile in order: a warp takes 32 rows, 8 columns of dK or dV and their 8 rotary partners.
-// Grid: HD / 16 CTAs for each border between two shares; the first one that cuts a tile stands for it.
+// Grid: HD / 16 CTAs for each border between two shares; the first one that cuts a tile stands for it. Bound by the
+// parts' way through L2: 16 us for 147 cuts of 128 KB each side, read cold.
 template <int HD>
 __global__ void __launch_bounds__(256) k_window_join(const WinBwdArgs p, const __grid_constant__ Split sp,
                                                      const float* __restrict__ parts) {
@@ -1234,8 +1249,8 @@ __global__ void __launch_bounds__(256) k_window_join(const WinBwdArgs p, const _
 
 // How the dK / dV work is dealt out. As many rounds of whole tiles as leave no CTA with more than its share; where
 // the tiles are as few as the SMs, a CTA each, if the longest of them takes no longer than equal shares and the
-// stores and the kernel that join them (about kJoin items: 4 sequences of 512 tokens take 65 us in whole
-// tiles of up to 16 items, 69 us in shares of 8.6).
+// stores and the kernel that join them (about kJoin items: the backward of 4 sequences of 512 tokens took 65 us in
+// whole tiles of up to 16 items, 69 us in shares of 8.6).
 constexpr int kJoin = 10;
 Split make_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
   const int64_t units = T / S * hkv;
