@@ -42,6 +42,13 @@ __device__ __forceinline__ void st_async_f2(uint32_t dst, float x, float y, uint
 __host__ __device__ inline float* row_terms(float* scratch) { return scratch + 4; }
 __host__ __device__ inline float* seq_weight(float* scratch, int64_t T) { return scratch + 4 + 4 * T; }
 
+// A value from L2, loaded here and not next to its use.
+__device__ __forceinline__ float load_cg(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // exp(d) - d - 1 without its cancellation near zero: the power series there
 __device__ __forceinline__ float k3_term(float d) {
   if (fabsf(d) < 0.125f) {
@@ -193,7 +200,7 @@ constexpr int kZeroBytes = 1024;
 //    brings into shared memory by bulk copies, in two halves of a ring of three. The consumers take a
 //    half to registers at once, so up to one and a half rows are in flight under a row's arithmetic,
 //    exchange and stores.
-//  - Consumer thread i holds slots i, i + consumers, ... of each half: NV of them, 4 NV logits, NV large
+//  - A consumer warp holds 32 NV / 2 neighbouring slots of each half, lane by lane, 4 NV logits a thread: NV large
 //    and the threads few, so that two slices fit an SM's registers without spills. With m its own
 //    maximum it forms e = 2^((x - m) log2 e) once; maxima and sums are merged by warp, CTA and cluster
 //    (st.async of each CTA's pair into its peers, onto their mbarrier), in a fixed order; the row's
@@ -207,6 +214,7 @@ template <int NV, int THREADS, int PER_SM>
 __global__ void __launch_bounds__(THREADS, PER_SM)
 k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int early) {
   static_assert(NV % 2 == 0 && kZeroBytes >= 128 * 8, "two halves; the zeros' space is reused");
+  constexpr int kRun = 32 * (NV / 2);  // slots of a warp in each half
   extern __shared__ __align__(16) float ring[];  // three halves of a slice
   __shared__ __align__(16) uint8_t zeros[kZeroBytes];
   __shared__ uint64_t full[3], empty[3], pair_bar[2];
@@ -346,19 +354,20 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int 
     const int off = (int)(reinterpret_cast<uintptr_t>(x) >> 2) & 3;
     const int b = z * slice, s1 = min((a.V + off + 3) / 4, b + slice);
     const bool dvec = (reinterpret_cast<uintptr_t>(d - off) & 7) == 0;
-    float w = 0.f;  // thread 0: the row's weight
-    if (threadIdx.x == 0) w = __ldcg(seq_weight(a.scratch, a.T) + (uint32_t)t / (uint32_t)a.S);
+    float w = 0.f;  // thread 0: the row's weight, under the arithmetic
+    if (threadIdx.x == 0) w = load_cg(seq_weight(a.scratch, a.T) + (uint32_t)t / (uint32_t)a.S);
     float v[4 * NV];
-    // this thread's slots: those n < NV / 2 with n * nc < mine[0], and as many of the second half
-    const int mine[2] = {min(half, s1 - b) - (int)threadIdx.x, s1 - b - half - (int)threadIdx.x};
+    // this thread's first slot of each half, and the half's slots from there on
+    const int at[2] = {warp * kRun + lane, half + warp * kRun + lane};
+    const int left[2] = {min(half, s1 - b) - at[0], s1 - b - at[1]};
 #pragma unroll
     for (int h = 0; h < 2; ++h, ++g) {
       if (h == 1 && !mbar_wait(&full[g % 3], (g / 3) & 1)) ok = false;
-      const float4* src = reinterpret_cast<const float4*>(ring + 4 * (g % 3) * half) + threadIdx.x;
+      const float4* src = reinterpret_cast<const float4*>(ring + 4 * (g % 3) * half) + at[0];
 #pragma unroll
       for (int n = 0; n < NV / 2; ++n) {
         float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (n * nc < mine[h]) q = src[n * nc];
+        if (32 * n < left[h]) q = src[32 * n];
         float* o = v + 4 * (h * (NV / 2) + n);
         o[0] = q.x;
         o[1] = q.y;
@@ -418,25 +427,42 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int 
     // no slot here holds a neighbour's logits, and the stores are aligned: nothing to look at a slot
     const bool whole = dvec && (b > 0 || off == 0) && 4 * s1 - off <= a.V;
     const float lse2 = factor.x, coef = factor.y, f = coef * ex2_approx(m - lse2);
+    const auto packed = [&](int n) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v[4 * n] * f, v[4 * n + 1] * f);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(v[4 * n + 2] * f, v[4 * n + 3] * f);
+      return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    };
+    if (whole) {
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int h = n / (NV / 2), k = (n - h * (NV / 2)) * nc;
-      if (k >= mine[h]) continue;
-      const __nv_bfloat162 g4[2] = {__floats2bfloat162_rn(v[4 * n] * f, v[4 * n + 1] * f),
-                                    __floats2bfloat162_rn(v[4 * n + 2] * f, v[4 * n + 3] * f)};
-      const int c = 4 * (b + h * half + k + (int)threadIdx.x) - off;
-      if (whole || (dvec && c >= 0 && c + 4 <= a.V)) {
-        *reinterpret_cast<uint2*>(d + c) = *reinterpret_cast<const uint2*>(g4);
-      } else {
-        const bf16* q = reinterpret_cast<const bf16*>(g4);
+      for (int h = 0; h < 2; ++h) {
+        uint2* dst = reinterpret_cast<uint2*>(d + 4 * (b + at[h]) - off);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c + e >= 0 && c + e < a.V) d[c + e] = q[e];
+        for (int n = 0; n < NV / 2; ++n) {
+          const uint2 g4 = packed(h * (NV / 2) + n);
+          if (32 * n < left[h]) dst[32 * n] = g4;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        const int h = n / (NV / 2), k = 32 * (n - h * (NV / 2));
+        const uint2 g4 = packed(n);
+        if (k >= left[h]) continue;
+        const int c = 4 * (b + at[h] + k) - off;
+        if (dvec && c >= 0 && c + 4 <= a.V) {
+          *reinterpret_cast<uint2*>(d + c) = g4;
+        } else {
+          const bf16* q = reinterpret_cast<const bf16*>(&g4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e >= 0 && c + e < a.V) d[c + e] = q[e];
+        }
       }
     }
     // the target's own element, by the thread that has just stored its slot
     const int ys = (y + off) / 4 - b;
-    if (ys >= 0 && ys < slice && (ys < half ? ys : ys - half) % nc == (int)threadIdx.x)
+    const int yh = ys < half ? ys : ys - half;  // its place in its half
+    if (ys >= 0 && ys < slice && yh / kRun == warp && yh % 32 == lane)
       d[y] = __float2bfloat16_rn(coef * (ex2_approx(fmaf(info[it & 3].xy, kLog2e, -lse2)) - 1.f));
   }
   if (z == 0 && ok)
@@ -510,7 +536,7 @@ cudaError_t launch_cluster(const PolicyArgs& a, int64_t row0, int64_t rows, int 
                            cudaStream_t s) {
   const auto kernel = k_policy_cluster<NV, THREADS, PER_SM>;
   const int half = (slice + 1) / 2;
-  const int threads = std::max(32, ((half + NV / 2 - 1) / (NV / 2) + 31) / 32 * 32) + 32, smem = 3 * half * 16;
+  const int run = 32 * (NV / 2), threads = std::max(1, (half + run - 1) / run) * 32 + 32, smem = 3 * half * 16;
   static std::atomic<unsigned long long> attr_done{0};
   if (!done_on_device(attr_done)) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
