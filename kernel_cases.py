@@ -12,6 +12,8 @@ Cases are the shapes of the Llama-3.1-8B-shaped layer at batch 4 x seq 512 (T = 
   dequant      NF4 -> bf16 of one 8B layer (218 M elements, 7 tensors)
   attn_fwd     causal GQA attention forward, 4 x 512, 32/8 heads, hd 128
   attn_bwd     its backward (D, dK/dV, dQ kernels)
+  attn_window_fwd / attn_window_bwd   the same under a window of 256 tokens with 4 sinks (the backward's
+               operations are those of its five products over the visible pairs)
   lora_u_qkv   LoRA projection U = s X Acat^T, X [2048, 4096], Acat [64, 4096]
   lora_u_down  the same for the down projection's input, X [2048, 14336]
   lora_v_gu    V = s dY Bexp, dY [2048, 28672], Bexp [28672, 64] (MN-major)
@@ -21,6 +23,8 @@ Cases are the shapes of the Llama-3.1-8B-shaped layer at batch 4 x seq 512 (T = 
                         launch, as a backward read issues them
   lora_grads_layer_sep  the same four groups as four launches
   ce           cross-entropy rows + dlogits over fp32 logits [2048, 128256]
+  policy       clipped policy loss with a KL term over the same logits, the second half of each sequence
+               counted: log-probabilities, loss, dlogits
   rmsnorm_fwd / rmsnorm_bwd   RMSNorm of the fp32 residual stream [2048, 4096] (bf16 output; the
                backward with the residual gradient added and a bf16 copy, as a layer uses it)
   swiglu_fwd / swiglu_bwd     SwiGLU of gate/up [2048, 2 x 14336] (the backward from fp32 dL/dm)
@@ -40,7 +44,9 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
-from layer_streamed_qlora_streaming_b200 import (k_attention_bwd, k_attention_fwd, k_cross_entropy, k_gemm, k_gemm_nf4,
+from layer_streamed_qlora_streaming_b200 import (POLICY_SEQ_MEAN, attention_window_scratch, k_attention_bwd, k_attention_fwd,
+                                                 k_attention_window_bwd, k_attention_window_fwd, k_cross_entropy, k_gemm,
+                                                 k_gemm_nf4, k_policy_loss, policy_scratch,
                                                  k_rmsnorm_bwd, k_rmsnorm_fwd, k_swiglu_bwd, k_swiglu_fwd,
                                                  k_lora_grads, k_lora_grads_multi, k_lora_skinny, k_nf4_dequant,
                k_nf4_quantize)
@@ -149,6 +155,24 @@ def build(case: str):
         def run():
             k_nf4_dequant(packed, qabs, gs, mean, n, out)
         return run, {"flop": None, "bytes": n * 0.5 + n / 64 + n * 2}
+    if case.startswith("attn_window"):
+        window, sinks, ld = 256, 4, (HQ + 2 * HKV) * HD
+        pairs = sum(i + 1 - max(0, i - window + 1 - sinks) for i in range(S))  # window + sinks at most
+        qkv, dqkv = _bf((T, ld), g), torch.empty(T, ld, dtype=torch.bfloat16, device="cuda")
+        q, k, v = qkv, qkv[:, HQ * HD:], qkv[:, (HQ + HKV) * HD:]
+        o, do = torch.empty(T, HQ * HD, dtype=torch.bfloat16, device="cuda"), _bf((T, HQ * HD), g)
+        lse = torch.empty(T, HQ, device="cuda")
+        scratch = torch.empty(attention_window_scratch(T, S, HQ, HKV, HD, window, sinks), device="cuda")
+
+        def fwd():
+            k_attention_window_fwd(q, ld, k, ld, v, ld, o, HQ * HD, lse, T, S, HQ, HKV, HD, window, sinks)
+
+        def bwd():
+            k_attention_window_bwd(q, ld, k, ld, v, ld, o, HQ * HD, do, HQ * HD, lse, scratch, dqkv, ld, dqkv[:, HQ * HD:],
+                                   ld, dqkv[:, (HQ + HKV) * HD:], ld, T, S, HQ, HKV, HD, window, sinks)
+        fwd()
+        flop = 4.0 * (T // S) * HQ * pairs * HD
+        return (fwd, {"flop": flop, "bytes": None}) if case == "attn_window_fwd" else (bwd, {"flop": 2.5 * flop, "bytes": None})
     if case.startswith("attn"):
         ld = (HQ + 2 * HKV) * HD
         qkv = _bf((T, ld), g)
@@ -213,6 +237,21 @@ def build(case: str):
         def run():
             k_cross_entropy(logits, T, V, tg, 1.0 / T, loss_rows, dlog)
         return run, {"flop": None, "bytes": T * V * 4 + T * V * 2}
+    if case == "policy":
+        V = VOCAB
+        logits = torch.randn(T, V, generator=g, device="cuda") * 2.0
+        tg = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+        mask = (torch.arange(T, device="cuda") % S >= S // 2).int()
+        old = torch.randn(T, generator=g, device="cuda") * 0.1 - 12.0
+        adv = torch.randn(T // S, generator=g, device="cuda")
+        logp, out = torch.empty(T, device="cuda"), torch.empty(4, device="cuda")
+        dlog = torch.empty(T, V, dtype=torch.bfloat16, device="cuda")
+        scratch = torch.empty(policy_scratch(T, S), device="cuda")
+
+        def run():
+            k_policy_loss(logits, T, V, tg, S, adv, logp, out, scratch, dlogits=dlog, old_logp=old, ref_logp=old, mask=mask,
+                          kl_beta=0.05, norm=POLICY_SEQ_MEAN, adv_per_seq=True)
+        return run, {"flop": None, "bytes": T // 2 * V * 4 + T * V * 2}
     raise SystemExit(f"unknown case {case}")
 
 

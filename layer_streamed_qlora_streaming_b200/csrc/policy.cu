@@ -205,11 +205,14 @@ constexpr int kZeroBytes = 1024;
 //    maximum it forms e = 2^((x - m) log2 e) once; maxima and sums are merged by warp, CTA and cluster
 //    (st.async of each CTA's pair into its peers, onto their mbarrier), in a fixed order; the row's
 //    factor coef 2^((m - lse) log2 e) then turns e into dlogits with one product.
-// Each logit crosses HBM once and takes one exponential. Bound by HBM: 4 + 2 bytes a logit, 2 bytes on
-// rows that do not count. 4096 rows of 151936 logits, most of them counted, take 467 us, 0.90 of the rate of a plain
-// copy; 2048 rows of 128256, half of them counted, 212 us, 0.76: clusters of 8 fill 264 of 296 places, and reads
-// and the uncounted rows' writes alternate; 999 rows of 32003, 28 us, 0.51: a row's chain of load, exchange
-// and stores comes three or four times for each CTA. (A CTA a row, read twice: 3896, 1461 and 75 us.)
+// Each logit crosses HBM once and takes one exponential. Bound by HBM: 4 + 2 bytes a logit, 2 bytes on rows that
+// do not count: 4096 rows of 151936 logits, most of them counted, take 453 us, 0.93 of the rate of a plain
+// copy; 2048 rows of 128256 265 us (0.91), with half of them counted 190 us (0.85); 999 rows of 32003, of which
+// less than half count, 27 us (0.53): a few rows a cluster, each a chain of load, exchange and stores.
+// (A CTA a row, read twice: 3896 us for the first, 1461 for the half counted, 75 for the last. The slots of a thread
+// as many apart as there are threads, each looked at: 2048 counted rows took 337 us instead of 265. dlogits by bulk
+// stores through shared memory, which leaves two halves to load into: 358. Rows in an order that mixes counted
+// ones with others: the half counted 196 instead of 190.)
 template <int NV, int THREADS, int PER_SM>
 __global__ void __launch_bounds__(THREADS, PER_SM)
 k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int early) {
