@@ -156,15 +156,19 @@ def _ptr(x) -> int | None:
     """Pointer of a torch tensor, numpy array, int address or None."""
     if x is None:
         return None
+    try:
+        stride = x.stride()
+    except AttributeError:
+        return _other_ptr(x)
+    # row-strided views are fine: every entry point takes explicit leading dimensions
+    if stride and stride[-1] != 1 and x.shape[-1] > 1:
+        raise ValueError("innermost dimension must be contiguous")
+    return x.data_ptr()
+
+
+def _other_ptr(x) -> int:
     if isinstance(x, int):
         return x
-    data_ptr = getattr(x, "data_ptr", None)
-    if data_ptr is not None:
-        # row-strided views are fine: every entry point takes explicit leading dimensions
-        stride = x.stride()
-        if stride and stride[-1] != 1 and x.shape[-1] > 1:
-            raise ValueError("innermost dimension must be contiguous")
-        return data_ptr()
     if hasattr(x, "ctypes"):
         if not x.flags["C_CONTIGUOUS"]:
             raise ValueError("array must be C-contiguous")
