@@ -104,10 +104,11 @@ lst_status lst_k_attention_bwd(const uint16_t* q, int64_t ldq, const uint16_t* k
  * when j <= i and (i - j < window or j < sinks); window >= S is plain causal attention. Long answers
  * are sampled this way, with a cache of the last `window` tokens and the first `sinks` ones; training
  * on them has to see the same keys. Arguments as lst_k_attention_fwd (any hq a multiple of hkv), o
- * 16-byte aligned with ldo a multiple of 8; window >= 1, sinks >= 0; T * hq below 2^31, T / S * hkv below 2^16. The
- * probabilities enter the P V product as bf16, so v has bf16's range. Rows of one sequence never
+ * 16-byte aligned with ldo a multiple of 8; window >= 1, sinks >= 0; S at most 2^30, T * hq below
+ * 2^31, T / S * hkv below 2^16. The probabilities enter the P V product as bf16, so v has bf16's
+ * range. Rows of one sequence never
  * reach another's result; within a sequence a NaN or infinity in k or v may reach queries that share
- * a 128-row tile with its visible ones. */
+ * a 128-row tile with its visible ones. No output overlaps an input. */
 lst_status lst_k_attention_window_fwd(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk,
                                       const uint16_t* v, int64_t ldv, uint16_t* o, int64_t ldo,
                                       float* lse, int64_t T, int32_t S, int32_t hq, int32_t hkv,
@@ -116,7 +117,7 @@ lst_status lst_k_attention_window_fwd(const uint16_t* q, int64_t ldq, const uint
 /* Its backward: dq, dk, dv bf16 (16-byte aligned, row strides multiples of 8) from dout and the
  * forward's o and lse; dk and dv add the query heads of their group. scratch: fp32
  * [lst_k_attention_window_scratch(...)], 16-byte aligned, not shared by calls that may overlap on the
- * GPU. Deterministic (no atomics). */
+ * GPU. No output overlaps an input or the scratch. Deterministic (no atomics). */
 lst_status lst_k_attention_window_bwd(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk,
                                       const uint16_t* v, int64_t ldv, const uint16_t* o, int64_t ldo,
                                       const uint16_t* dout, int64_t lddo, const float* lse,
@@ -167,7 +168,8 @@ lst_status lst_k_cross_entropy(const float* logits, int64_t T, int32_t V, const 
  * targets are not read for values. old_logp NULL: the policy is the one that sampled (r = 1).
  * ref_logp NULL: no KL term (kl_beta must be 0). A target out of range is reported (device error 2)
  * and its token adds nothing. V up to 2^20. scratch: fp32 [lst_k_policy_scratch(T, S)], 16-byte
- * aligned, not shared by calls that may overlap on the GPU. cfg: HOST memory. Deterministic. */
+ * aligned, not shared by calls that may overlap on the GPU. No output overlaps an input. cfg: HOST
+ * memory. Deterministic. */
 lst_status lst_k_policy_loss(const float* logits, int64_t T, int32_t V, const int32_t* targets, int32_t S,
                              const float* old_logp, const float* ref_logp, const float* adv,
                              const int32_t* mask, const lst_policy* cfg, float* logp, float* out,

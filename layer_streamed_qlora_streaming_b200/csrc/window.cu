@@ -329,7 +329,8 @@ struct TileWalk : QueryTile {
 // take 288 us, 0.55 of the matrix rate that a large product reaches, the tensor pipe 50 % active (an S of N = 64
 // takes 48 clocks an MMA where 32 would do: both operands come from shared memory); 4 x 512 tokens 17.7 us, 20 %
 // active: 512 CTAs of 2 to 7 blocks, each with a start and an end. (Persistent CTAs with the next tile's Q and K
-// under this one's end took 292 us against 287, and 18.0 us against 18.4.)
+// under this one's end took 292 us against 287, and 18.0 us against 18.4. Blocks of 128 keys with one buffer of S,
+// whose MMAs read Q half as often: 324 us, with two threads a row 336.)
 template <int HD>
 struct FwdCfg {
   static constexpr int KB = 64;  // keys of a block
