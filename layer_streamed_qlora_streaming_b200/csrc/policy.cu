@@ -220,14 +220,18 @@ constexpr int kZeroBytes = 1024;
 //    (st.async of each CTA's pair into its peers, onto their mbarrier), in a fixed order; the row's
 //    factor coef 2^((m - lse) log2 e) then turns e into dlogits with one product.
 // Each logit crosses HBM once and takes one exponential. Bound by HBM: 4 + 2 bytes a logit, 2 bytes on rows that
-// do not count: 4096 rows of 151936 logits, most of them counted, take 453 us, 0.93 of the rate of a plain
-// copy; 2048 rows of 128256 265 us (0.91), with half of them counted 190 us (0.85); 999 rows of 32003, of which
-// less than half count, 27 us (0.53): a few rows a cluster, each a chain of load, exchange and stores.
+// do not count: 4096 rows of 151936 logits, most of them counted, take 449 us, 0.93 of the rate of a plain
+// copy; 2048 rows of 128256 250 us (0.97), with half of them counted 182 us (0.88); 999 rows of 32003, of which
+// less than half count, 26 us (0.55): a few rows a cluster, each a chain of load, exchange and stores.
 // (A CTA a row, read twice: 3896 us for the first, 1461 for the half counted, 75 for the last. The slots of a thread
 // as many apart as there are threads, each looked at: 2048 counted rows took 337 us instead of 265. dlogits by bulk
 // stores through shared memory, which leaves two halves to load into: 358. Rows in an order that mixes counted
-// ones with others: the half counted 196 instead of 190.)
-template <int NV, int THREADS, int PER_SM>
+// ones with others: the half counted 196 instead of 190. Slices of half the size, on twice the CTAs: 8192 rows of
+// 32000 take 322 us instead of 301.)
+// ALIGNED: every row starts and ends with a slot (V a multiple of 4, the logits 16-byte aligned). Told apart for the
+// code around the stores: with the ends' code in it, 2048 rows of 128256 take 278 us instead of 250; without it,
+// each slot looked at, 4096 rows of 50257 take 257 us instead of 236.
+template <int NV, int THREADS, int PER_SM, bool ALIGNED>
 __global__ void __launch_bounds__(THREADS, PER_SM)
 k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int early) {
   static_assert(NV % 2 == 0 && kZeroBytes >= 128 * 8, "two halves; the zeros' space is reused");
@@ -313,7 +317,7 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int 
           continue;
         }
         const float* x = a.logits + lrow * a.V;
-        const int off = (int)(reinterpret_cast<uintptr_t>(x) >> 2) & 3, end = (a.V + off + 3) / 4;
+        const int off = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(x) >> 2) & 3, end = (a.V + off + 3) / 4;
         for (int h = 0; h < 2 && claim(); ++h, ++g) {
           const int k = g % 3;
           if (h == 0 && lane == i) info[it & 3] = r;
@@ -368,7 +372,7 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int 
     const int y = info[it & 3].y;
     const float* x = a.logits + lrow * a.V;
     bf16* d = a.dlog ? a.dlog + lrow * a.V : nullptr;
-    const int off = (int)(reinterpret_cast<uintptr_t>(x) >> 2) & 3;
+    const int off = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(x) >> 2) & 3;
     const int b = z * slice, s1 = min((a.V + off + 3) / 4, b + slice);
     const bool dvec = (reinterpret_cast<uintptr_t>(d - off) & 7) == 0;
     float w = 0.f;  // thread 0: the row's weight, under the arithmetic
@@ -441,45 +445,47 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int 
     }
     ok = named_all(1, nc, ok);  // a lost pair ends the loop for every consumer
     if (!d) continue;
-    // no slot here holds a neighbour's logits, and the stores are aligned: nothing to look at a slot
-    const bool whole = dvec && (b > 0 || off == 0) && 4 * s1 - off <= a.V;
     const float lse2 = factor.x, coef = factor.y, f = coef * ex2_approx(m - lse2);
     const auto packed = [&](int n) {
       const __nv_bfloat162 lo = __floats2bfloat162_rn(v[4 * n] * f, v[4 * n + 1] * f);
       const __nv_bfloat162 hi = __floats2bfloat162_rn(v[4 * n + 2] * f, v[4 * n + 3] * f);
       return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     };
-    if (whole) {
+    const int ys = (y + off) / 4 - b;
+    // slots [f0, f1) of the slice are all this row's
+    const int f0 = !ALIGNED && b == 0 && off ? 1 : 0, f1 = ALIGNED ? s1 - b : min(s1, (a.V + off) / 4) - b;
+    if (dvec) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint2* dst = reinterpret_cast<uint2*>(d + 4 * (b + at[h]) - off);
+        const int full = ALIGNED ? left[h] : (h ? f1 : min(half, f1)) - at[h];
 #pragma unroll
         for (int n = 0; n < NV / 2; ++n) {
           const uint2 g4 = packed(h * (NV / 2) + n);
-          if (32 * n < left[h]) dst[32 * n] = g4;
+          if (32 * n < full && (n > 0 || at[h] >= f0)) dst[32 * n] = g4;
         }
       }
-    } else {
+      if (!ALIGNED && warp == 0 && lane < 8) {  // the row's ends one by one
+        const int c = lane < 4 ? lane : 4 * (b + f1) - off + lane - 4;
+        if (lane < 4 ? f0 == 1 && lane < 4 - off && lane < a.V : f1 < s1 - b && c >= 0 && c < a.V)
+          d[c] = __float2bfloat16_rn(coef * (ex2_approx(fmaf(x[c], kLog2e, -lse2)) - (c == y ? 1.f : 0.f)));
+      }
+    } else {  // dlogits that lie otherwise than the logits modulo 16 bytes
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
         const int h = n / (NV / 2), k = 32 * (n - h * (NV / 2));
         const uint2 g4 = packed(n);
         if (k >= left[h]) continue;
         const int c = 4 * (b + at[h] + k) - off;
-        if (dvec && c >= 0 && c + 4 <= a.V) {
-          *reinterpret_cast<uint2*>(d + c) = g4;
-        } else {
-          const bf16* q = reinterpret_cast<const bf16*>(&g4);
+        const bf16* q = reinterpret_cast<const bf16*>(&g4);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e >= 0 && c + e < a.V) d[c + e] = q[e];
-        }
+        for (int e = 0; e < 4; ++e)
+          if (c + e >= 0 && c + e < a.V) d[c + e] = q[e];
       }
     }
     // the target's own element, by the thread that has just stored its slot
-    const int ys = (y + off) / 4 - b;
     const int yh = ys < half ? ys : ys - half;  // its place in its half
-    if (ys >= 0 && ys < slice && yh / kRun == warp && yh % 32 == lane)
+    if (ys >= (dvec ? f0 : 0) && ys < (dvec ? f1 : slice) && yh / kRun == warp && yh % 32 == lane)
       d[y] = __float2bfloat16_rn(coef * (ex2_approx(fmaf(info[it & 3].xy, kLog2e, -lse2)) - 1.f));
   }
   if (z == 0 && ok)
@@ -548,10 +554,10 @@ __global__ void __launch_bounds__(512) k_policy_rows(const PolicyArgs a, int64_t
 }
 
 // As many clusters as are resident at once (they take the rows in turn), at most one a row.
-template <int NV, int THREADS, int PER_SM>
-cudaError_t launch_cluster(const PolicyArgs& a, int64_t row0, int64_t rows, int cs, int slice, bool early,
-                           cudaStream_t s) {
-  const auto kernel = k_policy_cluster<NV, THREADS, PER_SM>;
+template <int NV, int THREADS, int PER_SM, bool ALIGNED>
+cudaError_t launch_cluster_as(const PolicyArgs& a, int64_t row0, int64_t rows, int cs, int slice, bool early,
+                              cudaStream_t s) {
+  const auto kernel = k_policy_cluster<NV, THREADS, PER_SM, ALIGNED>;
   const int half = (slice + 1) / 2;
   const int run = 32 * (NV / 2), threads = std::max(1, (half + run - 1) / run) * 32 + 32, smem = 3 * half * 16;
   static std::atomic<unsigned long long> attr_done{0};
@@ -587,6 +593,14 @@ cudaError_t launch_cluster(const PolicyArgs& a, int64_t row0, int64_t rows, int 
   const int64_t clusters = std::min<int64_t>(rows, fit.clusters);
   return launch_k(kernel, dim3((unsigned)(clusters * cs)), dim3((unsigned)threads), (size_t)smem, s, (unsigned)cs, a, row0,
                   rows, slice, early ? 1 : 0);
+}
+
+template <int NV, int THREADS, int PER_SM>
+cudaError_t launch_cluster(const PolicyArgs& a, int64_t row0, int64_t rows, int cs, int slice, bool early,
+                           cudaStream_t s) {
+  return a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0
+             ? launch_cluster_as<NV, THREADS, PER_SM, true>(a, row0, rows, cs, slice, early, s)
+             : launch_cluster_as<NV, THREADS, PER_SM, false>(a, row0, rows, cs, slice, early, s);
 }
 
 }  // namespace

@@ -150,6 +150,21 @@ def test_policy_variants():
     assert torch.equal(before, c.dlog)
 
 
+@pytest.mark.parametrize("V", [4096, 4099, 40000])
+def test_policy_dlogits_at_any_element(V):
+    # logits aligned, dlogits not: the same gradient, nothing around it touched
+    c = Case(2, 9, V)
+    c.run()
+    c.check()
+    n = c.T * V
+    for off in (1, 2, 3, 4, 5):
+        flat = torch.full((n + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+        c.run(dlogits=flat[off:off + n])
+        diff = (flat[off:off + n].float() - c.dlog[:n].float()).abs()
+        assert torch.all(diff <= 2 * U * c.dlog[:n].float().abs())  # (a row's ends are formed apart)
+        assert torch.all(flat[:off] == 7) and torch.all(flat[off + n:] == 7)
+
+
 def test_policy_masked_tokens_are_not_read():
     c = Case(4, 8, 300, "seq", 0.1, False)
     c.mask[8:16] = 0  # a sequence without a counted token
