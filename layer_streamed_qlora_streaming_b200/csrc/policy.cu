@@ -2,8 +2,8 @@
 // of Schulman et al., "Proximal Policy Optimization Algorithms", 2017, with the per-token KL estimate
 // k3 of Shao et al., "DeepSeekMath", 2024; formulas in policy.cuh). Its gradient:
 //   dl/dlogp = -r A [u is r A] + beta (1 - exp(ref - logp)),  dlogits = w dl/dlogp (onehot(y) - softmax(x)).
-// Each logit crosses HBM once: a cluster of CTAs holds a row in registers from its load to the store of
-// dlogits (k_policy_cluster); only rows too long for that are read twice (k_policy_rows).
+// Each logit crosses HBM once: a warp (k_policy_warp) or a cluster of CTAs (k_policy_cluster) holds a row in
+// registers from its load to the store of dlogits; only rows too long for that are read twice (k_policy_rows).
 #include "common.cuh"
 #include "pdl.cuh"
 #include "ex2.cuh"
@@ -178,12 +178,18 @@ __device__ __forceinline__ void finish_rows(const PolicyArgs& a, int done, int n
   __threadfence();
   const float4* rows = reinterpret_cast<const float4*>(row_terms(a.scratch));
   double s[4] = {0, 0, 0, 0};
-  for (int64_t i = threadIdx.x; i < a.T; i += nt) {
-    const float4 v = __ldcg(rows + i);
-    s[0] += v.x;
-    s[1] += v.y;
-    s[2] += v.z;
-    s[3] += v.w;
+  constexpr int kAhead = 8;  // loads under way at once: one after another they take most of a call on many short rows
+  for (int64_t i = threadIdx.x; i < a.T; i += kAhead * nt) {
+    float4 v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) v[u] = i + u * nt < a.T ? __ldcg(rows + i + u * nt) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      s[0] += v[u].x;
+      s[1] += v[u].y;
+      s[2] += v[u].z;
+      s[3] += v[u].w;
+    }
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -220,9 +226,9 @@ constexpr int kZeroBytes = 1024;
 //    (st.async of each CTA's pair into its peers, onto their mbarrier), in a fixed order; the row's
 //    factor coef 2^((m - lse) log2 e) then turns e into dlogits with one product.
 // Each logit crosses HBM once and takes one exponential. Bound by HBM: 4 + 2 bytes a logit, 2 bytes on rows that
-// do not count: 4096 rows of 151936 logits, most of them counted, take 449 us, 0.93 of the rate of a plain
-// copy; 2048 rows of 128256 250 us (0.97), with half of them counted 182 us (0.88); 999 rows of 32003, of which
-// less than half count, 26 us (0.55): a few rows a cluster, each a chain of load, exchange and stores.
+// do not count: 4096 rows of 151936 logits, most of them counted, take 443 us, 0.95 of the rate of a plain
+// copy; 2048 rows of 128256 250 us (0.97), with half of them counted 179 us (0.90); 999 rows of 32003, of which
+// less than half count, 25 us (0.57): a few rows a cluster, each a chain of load, exchange and stores.
 // (A CTA a row, read twice: 3896 us for the first, 1461 for the half counted, 75 for the last. The slots of a thread
 // as many apart as there are threads, each looked at: 2048 counted rows took 337 us instead of 265. dlogits by bulk
 // stores through shared memory, which leaves two halves to load into: 358. Rows in an order that mixes counted
@@ -494,6 +500,108 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int 
   cluster_sync_all();  // no CTA leaves before its peers have their pairs
 }
 
+// Short rows, a warp each (slots as above, slot lane + 32 k in the lane's registers): no exchange, and as many
+// rows in flight as the warps of all SMs. Bound by latency (a row's loads and merge, then the sum of the rows'
+// terms): 128 rows of 512 logits 6.1 us, where clusters take 8.4; 3344 rows of 1427 14.5 against 25, of 4000
+// (the longest: 32 slots a lane leave three CTAs an SM) 21 against 27.
+template <int NV>
+__global__ void __launch_bounds__(128, NV <= 4 ? 10 : NV <= 16 ? 5 : 3) k_policy_warp(const PolicyArgs a, int64_t row0, int64_t rows, int early) {
+  if (!early) pdl_wait();
+  pdl_trigger();
+  __shared__ double part[128];
+  const int lane = threadIdx.x & 31;
+  const int64_t lrow = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), t = row0 + lrow;
+  if (lrow < rows) {
+    const float* x = a.logits + lrow * a.V;
+    bf16* d = a.dlog ? a.dlog + lrow * a.V : nullptr;
+    const int off = (int)(reinterpret_cast<uintptr_t>(x) >> 2) & 3, n = (a.V + off + 3) / 4;
+    const bool dvec = (reinterpret_cast<uintptr_t>(d - off) & 7) == 0;
+    const int y = a.y[t];
+    bool live = !a.mask || a.mask[t] != 0;
+    if (live && (y < 0 || y >= a.V)) {
+      if (lane == 0) dev_fail(DEV_ERR_BAD_INDEX);
+      live = false;
+    }
+    float v[4 * NV], m = 0.f, lse2 = 0.f, coef = 0.f, xy = 0.f;
+    if (live) {
+      const int seq = (int)((uint32_t)t / (uint32_t)a.S);
+      const float adv = a.adv[a.adv_per_seq ? seq : t], old = a.old_logp ? a.old_logp[t] : 0.f;
+      const float ref = a.ref_logp ? a.ref_logp[t] : 0.f;
+      xy = x[y];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = lane + 32 * k, c = 4 * i - off;
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (i < n) {
+          if (c >= 0 && c + 4 <= a.V) {
+            q = *reinterpret_cast<const float4*>(x + c);
+          } else {
+            if (c >= 0) q.x = x[c];
+            if (c + 1 >= 0 && c + 1 < a.V) q.y = x[c + 1];
+            if (c + 2 >= 0 && c + 2 < a.V) q.z = x[c + 2];
+            if (c + 3 < a.V) q.w = x[c + 3];
+          }
+        }
+        v[4 * k] = q.x, v[4 * k + 1] = q.y, v[4 * k + 2] = q.z, v[4 * k + 3] = q.w;
+      }
+      float m4[4] = {v[0], v[1], v[2], v[3]}, s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 4; k < 4 * NV; ++k) m4[k & 3] = fmaxf(m4[k & 3], v[k]);
+      m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      m = m > -INFINITY ? m * kLog2e : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4 * NV; ++k) {
+        v[k] = ex2_approx(fmaf(v[k], kLog2e, -m));
+        s4[k & 3] += v[k];
+      }
+      const float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      if (s == 0.f) m = -INFINITY;
+      const float rm = warp_max_of(m), l2 = log2f(lane_sum<32>(m > -INFINITY ? s * ex2_approx(m - rm) : s));
+      lse2 = rm + l2;
+      const float logp = (fmaf(xy, kLog2e, -rm) - l2) * kLn2;
+      const Token k = policy_token(a, adv, old, ref, logp);
+      pdl_wait();
+      const float w = load_cg(seq_weight(a.scratch, a.T) + seq);
+      coef = -w * k.slope;
+      if (lane == 0) {
+        a.logp[t] = logp;
+        reinterpret_cast<float4*>(row_terms(a.scratch))[t] =
+            make_float4(w * k.terms.x, w * k.terms.y, w * k.terms.z, w * k.terms.w);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4 * NV; ++k) v[k] = 0.f;
+      if (lane == 0) {
+        a.logp[t] = 0.f;
+        reinterpret_cast<float4*>(row_terms(a.scratch))[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    if (d) {
+      const float f = live ? coef * ex2_approx(m - lse2) : 0.f;
+      const bf16 gy = __float2bfloat16_rn(coef * (ex2_approx(fmaf(xy, kLog2e, -lse2)) - 1.f));
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = lane + 32 * k, c = 4 * i - off;
+        if (i >= n) continue;
+        bf16 g[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = live && c + e == y ? gy : __float2bfloat16_rn(v[4 * k + e] * f);
+        if (dvec && c >= 0 && c + 4 <= a.V) {
+          const __nv_bfloat162 lo(g[0], g[1]), hi(g[2], g[3]);
+          *reinterpret_cast<uint2*>(d + c) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e >= 0 && c + e < a.V) d[c + e] = g[e];
+        }
+      }
+    }
+  }
+  pdl_wait();  // the count of rows done is set to zero in front
+  __syncthreads();
+  finish_rows(a, (int)min((int64_t)4, rows - (int64_t)blockIdx.x * 4), 128, part);
+}
+
 // Rows longer than a cluster's registers (V above 300,000): one CTA a row, read twice.
 __global__ void __launch_bounds__(512) k_policy_rows(const PolicyArgs a, int64_t row0) {
   pdl_wait();
@@ -633,7 +741,12 @@ cudaError_t policy_rows(const PolicyArgs& a, int64_t row0, int64_t rows, bool ea
   while (cs < 8 && ((slots + cs - 1) / cs > 4750 || (rows * cs < 2 * device_sm_count() && slots / cs > 1024))) cs *= 2;
   const int slice = (slots + cs - 1) / cs;
   cudaError_t e;
-  if (slice <= 512) e = launch_cluster<2, 288, 4>(a, row0, rows, cs, slice, early, s);
+  const auto warps = [&](auto kernel) {
+    return launch_k(kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, 0, a, row0, rows, early ? 1 : 0);
+  };
+  if (slots <= 32 * 4) e = warps(k_policy_warp<4>);
+  else if (slots <= 32 * 16) e = warps(k_policy_warp<16>);
+  else if (slots <= 32 * 32) e = warps(k_policy_warp<32>);
   else if (slice <= 1536) e = launch_cluster<6, 288, 4>(a, row0, rows, cs, slice, early, s);
   else if (slice <= 4750) e = launch_cluster<22, 256, 2>(a, row0, rows, cs, slice, early, s);
   else if (slice <= 9400) e = launch_cluster<22, 512, 1>(a, row0, rows, cs, slice, early, s);

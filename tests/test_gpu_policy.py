@@ -110,6 +110,11 @@ class Case:
     (2, 3, 2, False, 0.1, 1),
     (4, 32, 512, True, 0.1, 0),
     (3, 17, 1001, False, 0.0, 3),     # odd vocabulary, odd base
+    (2, 9, 509, True, 0.1, 2),        # the longest rows of a warp's variants and the next ones
+    (2, 9, 2044, False, 0.1, 0),
+    (3, 7, 2047, True, 0.1, 1),
+    (2, 9, 4092, True, 0.1, 0),
+    (2, 9, 4094, False, 0.1, 3),
     (2, 9, 16384, True, 0.1, 2),
     (1, 40, 32003, False, 0.1, 0),
     (5, 1, 4099, False, 0.5, 1),      # sequences of one token
@@ -165,8 +170,9 @@ def test_policy_dlogits_at_any_element(V):
         assert torch.all(flat[:off] == 7) and torch.all(flat[off + n:] == 7)
 
 
-def test_policy_masked_tokens_are_not_read():
-    c = Case(4, 8, 300, "seq", 0.1, False)
+@pytest.mark.parametrize("V", [300, 5001])
+def test_policy_masked_tokens_are_not_read(V):
+    c = Case(4, 8, V, "seq", 0.1, False)
     c.mask[8:16] = 0  # a sequence without a counted token
     c.tmask.copy_(torch.from_numpy(c.mask))
     off = torch.from_numpy(c.mask == 0).cuda()
@@ -187,9 +193,10 @@ def test_policy_masked_tokens_are_not_read():
         assert torch.all(c.out[:4] == 0) and torch.all(c.dlog[:c.T * c.V] == 0) and torch.all(c.logp[:c.T] == 0)
 
 
-def test_policy_words_that_are_ruled_out():
+@pytest.mark.parametrize("V", [1000, 5000])
+def test_policy_words_that_are_ruled_out(V):
     # -inf logits (words a sampler was not allowed to draw) take no probability and no gradient
-    c = Case(2, 10, 5000, "token", 0.1)
+    c = Case(2, 10, V, "token", 0.1)
     ban = np.random.default_rng(1).uniform(size=c.x.shape) < 0.9
     ban[np.arange(c.T), c.y] = False
     c.x[ban] = -np.inf
@@ -206,11 +213,12 @@ def test_policy_words_that_are_ruled_out():
     assert torch.all(c.dlog[:c.T * c.V].view(c.T, c.V)[torch.from_numpy(ban).cuda()] == 0)
 
 
-def test_policy_bad_target_is_reported_and_adds_nothing():
-    c = Case(2, 6, 100, "fixed", 0.1, keep=1.1)
+@pytest.mark.parametrize("V", [100, 6000])
+def test_policy_bad_target_is_reported_and_adds_nothing(V):
+    c = Case(2, 6, V, "fixed", 0.1, keep=1.1)
     c.run()
     torch.cuda.synchronize()
-    c.ty[3] = 100
+    c.ty[3] = V
     c.ty[7] = -1
     c.run()
     torch.cuda.synchronize()
@@ -219,8 +227,9 @@ def test_policy_bad_target_is_reported_and_adds_nothing():
     c.check()
 
 
-def test_policy_two_streams_and_a_graph():
-    cs = [Case(3, 16, 9000, "seq", 0.1, seed=s) for s in range(2)]
+@pytest.mark.parametrize("V", [900, 9000])
+def test_policy_two_streams_and_a_graph(V):
+    cs = [Case(3, 16, V, "seq", 0.1, seed=s) for s in range(2)]
     for c in cs:
         c.run()
     torch.cuda.synchronize()
