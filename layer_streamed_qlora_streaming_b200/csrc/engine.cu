@@ -776,6 +776,7 @@ lst_status layer_fwd(lst_ctx* c, int i, const uint8_t* blob, const uint8_t* hdr,
       static_cast<AttnArgs&>(w) = a;
       w.window = c->win;
       w.sinks = c->sinks;
+      w.parts = 2;  // a step has no fewer bits under a window than without one
       CK(window_fwd(w, c->stream));
     } else {
       CK(attention_fwd(a, c->stream));

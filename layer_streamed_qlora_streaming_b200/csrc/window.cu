@@ -10,8 +10,9 @@
 // visible pair: the forward, dQ (which forms D first), and dK / dV, whose work is cut into equal shares; a
 // fourth adds the parts of what was cut.
 // Tiles come by 3D TMA maps (column, row of the sequence, sequence): rows behind a sequence read as
-// zeros, never as the next sequence. P and dS are rounded to bf16 as operands (half a step of 2^-8
-// relative, independent of the output's own rounding); everything else is fp32.
+// zeros, never as the next sequence. Operands of products are bf16: q, k, v, dout as given, dS and the
+// backward's P rounded (half a step of 2^-8 relative each, independent of the output's own rounding), the
+// forward's P rounded too or held in two bf16 parts (WinArgs::parts). Scores, lse, sums and products are fp32.
 #include "common.cuh"
 #include "pdl.cuh"
 #include "ex2.cuh"
@@ -339,7 +340,12 @@ struct FwdCfg {
   static constexpr uint32_t SMEM = TILE + 4 * KT + 1024 + 256;
 };
 
-template <int HD>
+// PARTS 2: what the rounding of P to bf16 leaves goes behind it as a second bf16 value and takes a product of its own,
+// so that 16 bits of P count (the causal kernel's fp16 has 11, at the price of v's range). Where only the output's
+// 8 bits matter, as in a call of the kernel by itself, one part is enough: 16384 tokens as above take 366 us in two
+// parts against 293 in one, 4 x 512 19.6 against 17.8. The engine's steps take two, which
+// their copies hide: with one, a window would cost a stack of layers bits that the causal kernel keeps.
+template <int HD, int PARTS>
 __global__ void __launch_bounds__(192, 2)
 k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmK16,
@@ -425,7 +431,9 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       if (!(ok = warp_wait(v_full + s, (j >> 1) & 1) && warp_wait(p_full + s, (j >> 1) & 1))) break;
       tc_fence_after();
       if (elect_one()) {  // O += P_j V_j
-        mma_ts<kKB, 0>(tO, tS + s * kKB, make_desc(smem_u32(sV + s * C::KT), C::KCH, 1024), idO, kb.width(j), j > 0);
+        const Desc v = make_desc(smem_u32(sV + s * C::KT), C::KCH, 1024);
+        mma_ts<kKB, 0>(tO, tS + s * kKB, v, idO, kb.width(j), j > 0);
+        if (PARTS == 2) mma_ts<kKB, 0>(tO, tS + s * kKB + kKB / 2, v, idO, kb.width(j), true);
         umma_commit(j + 1 < kb.n ? v_empty + s : o_full);
       }
       __syncwarp();
@@ -481,7 +489,7 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
       }
       const float mm = m > -INFINITY ? m : 0.f;  // a row that sees nothing so far
       uint64_t ps[2] = {0, 0};
-      uint32_t w[kKB / 2];
+      uint32_t w[PARTS * kKB / 2];
       const uint64_t sl = f2(sl2, sl2), mn = f2(-mm, -mm);
 #pragma unroll
       for (int c = 0; c < kKB / 2; ++c) {
@@ -489,12 +497,16 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         ex2_pair(fma2(f2(x[2 * c], x[2 * c + 1]), sl, mn), a0, a1);
         ps[c & 1] = add2(ps[c & 1], f2(a0, a1));
         w[c] = pack2(a0, a1);
+        if constexpr (PARTS == 2) {  // what the rounding leaves, exact in fp32
+          unpack(fma2(f2(__uint_as_float(w[c] << 16), __uint_as_float(w[c] & 0xffff0000u)), f2(-1.f, -1.f), f2(a0, a1)), a0, a1);
+          w[kKB / 2 + c] = pack2(a0, a1);
+        }
       }
       float l0, l1;
       unpack(add2(ps[0], ps[1]), l0, l1);
       l += l0 + l1;
-      tmem_st16(tX, w);
-      tmem_st16(tX + 16, w + 16);
+#pragma unroll
+      for (int c = 0; c < PARTS * kKB / 2; c += 16) tmem_st16(tX + c, w + c);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(p_full + (j & 1));
@@ -1339,7 +1351,7 @@ cudaError_t allow_smem(K* kernel, uint32_t bytes, std::atomic<unsigned long long
   return e;
 }
 
-template <int HD>
+template <int HD, int PARTS>
 cudaError_t launch_fwd(const WinArgs& a, cudaStream_t s) {
   using C = FwdCfg<HD>;
   const int64_t B = a.T / a.S, cq = (int64_t)a.hq * HD, ck = (int64_t)a.hkv * HD;
@@ -1349,10 +1361,10 @@ cudaError_t launch_fwd(const WinArgs& a, cudaStream_t s) {
       !make_map3(&v16, a.v, B, a.S, ck, a.ldv, 16) || !make_map3(&o, a.o, B, a.S, cq, a.ldo, kQB))
     return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(k_window_fwd<HD>, C::SMEM, done);
+  const cudaError_t e = allow_smem(k_window_fwd<HD, PARTS>, C::SMEM, done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = B * a.hq * ((a.S + kQB - 1) / kQB);
-  return launch_k(k_window_fwd<HD>, dim3((unsigned)tiles), dim3(192), C::SMEM, s, 0, q, k, v, k16, v16, o, a,
+  return launch_k(k_window_fwd<HD, PARTS>, dim3((unsigned)tiles), dim3(192), C::SMEM, s, 0, q, k, v, k16, v16, o, a,
                   2 * device_sm_count());
 }
 
@@ -1406,7 +1418,8 @@ cudaError_t window_fwd(WinArgs a, cudaStream_t s) {
   a.window = std::min(a.window, a.S);
   a.sinks = std::min(a.sinks, a.S);
   a.heads = (int)(a.T / a.S) * a.hq;
-  const cudaError_t e = a.hd == 128 ? launch_fwd<128>(a, s) : launch_fwd<64>(a, s);
+  const cudaError_t e = a.parts == 2 ? (a.hd == 128 ? launch_fwd<128, 2>(a, s) : launch_fwd<64, 2>(a, s))
+                                     : (a.hd == 128 ? launch_fwd<128, 1>(a, s) : launch_fwd<64, 1>(a, s));
   note_launch(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -7,8 +7,9 @@ namespace lst {
 
 // Key j of a sequence is visible to its query i when j <= i and (i - j < window or j < sinks).
 struct WinArgs : AttnArgs {
-  int window;  // >= 1
-  int sinks;   // >= 0
+  int window;     // >= 1
+  int sinks;      // >= 0
+  int parts = 1;  // bf16 values that hold a probability in P V: 1 (8 bits) or 2 (16 bits)
   int heads;   // T / S * hq, set by window_fwd (window_bwd)
 };
 struct WinBwdArgs : AttnBwdArgs {  // D: window_scratch() floats, 16-byte aligned
