@@ -10,7 +10,8 @@
 // visible pair: the forward, dQ (which forms D first), and dK / dV, whose work is cut into equal shares; a
 // fourth adds the parts of what was cut.
 // Tiles come by 3D TMA maps (column, row of the sequence, sequence): rows behind a sequence read as
-// zeros, never as the next sequence. Operands of products are bf16: q, k, v, dout as given, dS and the
+// zeros, never as the next sequence. D is formed from the unrounded o where the caller has it (AttnArgs::o32,
+// AttnBwdArgs::o32), else from the bf16 one. Operands of products are bf16: q, k, v, dout as given, dS and the
 // backward's P rounded (half a step of 2^-8 relative each, independent of the output's own rounding), the
 // forward's P rounded too or held in two bf16 parts (WinArgs::parts). Scores, lse, sums and products are fp32.
 #include "common.cuh"
@@ -529,6 +530,12 @@ k_window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 #pragma unroll
         for (int e = 0; e < 32; ++e) w[e] = pack2(y[2 * e], y[2 * e + 1]);
         stage_row(sQ + c / 64 * C::CH, r, w);
+        if (p.o32 && i < p.S) {  // for the backward's D
+          float4* dst = reinterpret_cast<float4*>(p.o32 + (t * p.hq + h) * HD + c);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        }
+        __syncwarp();
       }
       fence_proxy_async();
     }
@@ -614,7 +621,9 @@ struct DqCfg {
   static constexpr uint32_t SMEM = 7 * TILE + 256 + 4 * kQB * 4;
 };
 
-template <int HD>
+// O32: D from the unrounded o (told apart for the registers: with the choice made in the kernel, calls without it took
+// 1 % longer).
+template <int HD, bool O32>
 __global__ void __launch_bounds__(320, 1)
 k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
             const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -692,7 +701,9 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       for (int j = -1; j < kb.n; ++j, ++entry, advance(1)) {  // -1: o
         if (entry >= C::NK && !(ok = warp_wait(k_empty + slot, par ^ 1))) break;
         if (elect_one()) {
-          if (j < 0) {
+          if (O32 && j < 0) {
+            mbar_arrive(k_full + slot);
+          } else if (j < 0) {
             mbar_arrive_expect_tx(k_full + slot, C::TILE);
             load_tile<HD>(sK + slot * C::TILE, C::CH, &tmFo, k_full + slot, tile.h * HD, tile.q0, tile.b);
           } else {
@@ -766,7 +777,9 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
       return tile.q0 + r < p.S ? p.lse[((int64_t)tile.b * p.S + tile.q0 + r) * p.hq + tile.h] : INFINITY;
     };
     // the first four warps copy Q's rows of tile `n` into TMEM, the others dO's; each of them forms D = dO . o over
-    // half of the columns
+    // half of the columns, o unrounded where it is given: the rounding of o takes dO . (o - bf16 o) from D, and dq
+    // then has that times the row's mean key (keys and values with offsets of 4: the q adapter's gradients were off by
+    // 0.19 of their largest value, instead of 0.004)
     const auto copy = [&](int n) {
       if (!warp_wait2(q_full, n & 1, k_full + slot, par)) return false;
       const auto row = [&](const uint8_t* t, int e) {  // columns [8 e, 8 e + 8)
@@ -780,15 +793,32 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
         tmem_st32(tA + g * 64 + c * 32 + lanes, w);
       }
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int e = 0; e < HD / 16; ++e) {
-        const uint4 d4 = *row(sO, g * (HD / 16) + e), o4 = *row(sK + slot * C::TILE, g * (HD / 16) + e);
-        const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w}, o[4] = {o4.x, o4.y, o4.z, o4.w};
+      const auto dot = [&](int e, const float2 (&o)[4]) {  // over columns [8 e, 8 e + 8) of this half
+        const uint4 d4 = *row(sO, g * (HD / 16) + e);
+        const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float2 d2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(d + u));
-          const float2 o2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(o + u));
-          sum[u] = fmaf(d2.x, o2.x, fmaf(d2.y, o2.y, sum[u]));
+          sum[u] = fmaf(d2.x, o[u].x, fmaf(d2.y, o[u].y, sum[u]));
+        }
+      };
+      if constexpr (!O32) {
+#pragma unroll
+        for (int e = 0; e < HD / 16; ++e) {
+          const uint4 o4 = *row(sK + slot * C::TILE, g * (HD / 16) + e);
+          const uint32_t w[4] = {o4.x, o4.y, o4.z, o4.w};
+          float2 o[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) o[u] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(w + u));
+          dot(e, o);
+        }
+      } else {
+        const int64_t t = (int64_t)tile.b * p.S + min(tile.q0 + r, p.S - 1);
+        const float4* src = reinterpret_cast<const float4*>(p.o32 + (t * p.hq + tile.h) * HD + g * (HD / 2));
+#pragma unroll
+        for (int e = 0; e < HD / 16; ++e) {
+          const float4 a = src[2 * e], b = src[2 * e + 1];
+          dot(e, {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)});
         }
       }
       sD[((n & 1) * 2 + g) * kQB + r] = tile.q0 + r < p.S ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
@@ -1381,12 +1411,13 @@ cudaError_t launch_bwd(const WinBwdArgs& a, cudaStream_t s) {
       !make_map3(&dk, a.dk, B, a.S, ck, a.lddk, kQB) ||
       !make_map3(&dv, a.dv, B, a.S, ck, a.lddv, kQB))
     return cudaErrorInvalidValue;
-  static std::atomic<unsigned long long> done_q{0}, done_k{0};
-  cudaError_t e = allow_smem(k_window_dq<HD>, Q::SMEM, done_q);
+  static std::atomic<unsigned long long> done_q[2] = {{0}, {0}}, done_k{0};
+  const auto dq_kernel = a.o32 ? k_window_dq<HD, true> : k_window_dq<HD, false>;
+  cudaError_t e = allow_smem(dq_kernel, Q::SMEM, done_q[a.o32 != nullptr]);
   if (e == cudaSuccess) e = allow_smem(k_window_dkdv<HD>, K::SMEM, done_k);
   if (e != cudaSuccess) return e;
   const int tiles = (int)(B * a.hq * ((a.S + kQB - 1) / kQB));
-  e = launch_k(k_window_dq<HD>, dim3((unsigned)std::min(tiles, device_sm_count())), dim3(320), Q::SMEM, s, 0, q, o, k, v, k16,
+  e = launch_k(dq_kernel, dim3((unsigned)std::min(tiles, device_sm_count())), dim3(320), Q::SMEM, s, 0, q, o, k, v, k16,
                v16, dq, fo, a, tiles);
   note_launch(1);
   if (e != cudaSuccess) return e;

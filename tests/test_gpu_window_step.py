@@ -72,3 +72,17 @@ def test_probabilities_keep_sixteen_bits(wl, window, sinks):
     o = P @ v
     tol = U * o.abs() + (U * U + 2 * e) * (P @ v.abs())
     assert ((heads(got) - o).abs() / tol).max().item() <= 1.0
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 0), (40, 4)])
+@pytest.mark.parametrize("wl", [LAYER.with_(batch=2, seq=100, qkv_bias=True), WIDE.with_(batch=1, seq=200, qkv_bias=True)],
+                         ids=["hd64", "hd128"])
+def test_gradients_with_keys_and_values_far_from_zero(wl, window, sinks):
+    # D has to match P's normalisation: from the rounded o it is off by do . (o - bf16 o), and dq by that times the mean
+    # key. Offsets of 4 in k and v (a q/k/v bias) make that 0.19 of the q gradients' largest value.
+    inp = build_inputs(wl)
+    r = np.random.default_rng(1)
+    bias = inp["raw"][0]["bias"]
+    for p in ("k", "v"):
+        bias[p] = (bias[p] + 4 * np.sign(r.normal(size=bias[p].shape))).astype(np.float32)
+    _hidden_step(wl, inp, window, sinks)
