@@ -435,7 +435,7 @@ def _forward(x, Ws, lora, sh):
 
 
 def dpo_step(wl, raw_layers, head, tokens, targets, npairs, beta, mask=None, blobs=None, bf16_acts=False,
-             lora=None):
+             lora=None, window=0, sinks=0):
     """Loss and LoRA gradients of one DPO step on 2 * npairs sequences of wl.seq tokens.
 
     The reference pass runs every layer with the adapters off (B = 0 makes the side path exactly
@@ -444,7 +444,7 @@ def dpo_step(wl, raw_layers, head, tokens, targets, npairs, beta, mask=None, blo
     Returns dict(loss, grads, pi, ref).
     """
     L = wl.n_layers
-    sh = Shape(wl, bf16_acts)
+    sh = Shape(wl, bf16_acts, window, sinks)
     nseq, S = 2 * npairs, wl.seq
     assert nseq == wl.batch
     if blobs is None:

@@ -86,3 +86,74 @@ def test_gradients_with_keys_and_values_far_from_zero(wl, window, sinks):
     for p in ("k", "v"):
         bias[p] = (bias[p] + 4 * np.sign(r.normal(size=bias[p].shape))).astype(np.float32)
     _hidden_step(wl, inp, window, sinks)
+
+
+def _parts(wl, window, sinks):
+    """fp32 values that the dK / dV kernel leaves for the kernel that joins the parts of cut key tiles."""
+    n = lst.attention_window_scratch(wl.tokens, wl.seq, wl.n_heads, wl.n_kv_heads, wl.head_dim, window, sinks)
+    return n - 2 * wl.batch * wl.n_heads * -(-wl.seq // 128) * 128  # without (lse, D) of every query
+
+
+@pytest.mark.parametrize("wl,window,sinks,cut", [
+    (WIDE.with_(batch=1, seq=1500), 256, 4, True),      # key tiles cut into shares, joined
+    (LAYER.with_(batch=1, seq=1100), 300, 130, True),   # sinks that cross a tile
+    (WIDE.with_(batch=2, seq=300), 200, 4, False)])     # whole key tiles
+def test_rotary_embedding_undone_in_every_tile(wl, window, sinks, cut):
+    # only a step undoes the embedding in dq and dk; far positions and the joined tiles have their own code for it
+    assert (_parts(wl, window, sinks) > 0) == cut
+    _hidden_step(wl, build_inputs(wl), window, sinks)
+
+
+@pytest.mark.parametrize("window,sinks", [(17, 4), (5, 0)])
+def test_dpo_step_under_a_window(window, sinks):
+    wl = syn.WORKLOADS["tiny"].with_(batch=4, n_kv_heads=2)
+    inp = build_inputs(wl)
+    toks, tgts, mask = syn.preference_pairs(wl)
+    ctx = make_context(wl, inp, streamed=True)
+    ctx.set_attention_window(window, sinks)
+    grads = np.zeros(ctx.lora_numel(), dtype=np.float32)
+    loss = ctx.step_dpo(toks, tgts, mask, wl.batch // 2, wl.seq, 0.5, grads)
+    ref = M.dpo_step(wl, inp["raw"], inp["head"], toks, tgts, wl.batch // 2, 0.5, mask=mask, bf16_acts=True, window=window,
+                     sinks=sinks)
+    assert abs(loss - ref["loss"]) <= LOSS_RTOL * abs(ref["loss"])
+    _check_grads(ctx, grads, ref["grads"])
+    ctx.close()
+
+
+def test_window_and_lengths_that_change_between_steps():
+    # the backward's scratch grows with the steps; a step's bytes do not depend on the ones before it
+    wl = WIDE.with_(batch=2, seq=700)
+    inp = build_inputs(wl)
+    ctx = make_context(wl, inp, streamed=True)
+    grads = {}
+
+    def step(batch, seq, window, sinks):
+        g = np.zeros(ctx.lora_numel(), dtype=np.float32)
+        ctx.set_attention_window(window, sinks)
+        n = batch * seq
+        ctx.step_hidden(syn.to_bf16_bits(inp["x"][:n]), syn.to_bf16_bits(inp["G"][:n]), batch, seq, g)
+        return g.tobytes()
+
+    runs = [(1, 9, 3, 0), (2, 700, 100, 4), (1, 700, 700, 0), (2, 700, 30, 200), (2, 64, 5, 5)]
+    for i in (0, 1, 2, 3, 4, 2, 0, 3, 1):
+        assert grads.setdefault(i, step(*runs[i])) == step(*runs[i])
+    ctx.close()
+
+
+@pytest.mark.slow
+def test_32b_shaped_layers_under_a_window():
+    # the layers whose top q / k gradients are the most sensitive to rounding: the bound of the causal path
+    wl = syn.WORKLOADS["qwen32b"].with_(n_layers=2, batch=1, seq=256)
+    inp = build_inputs(wl)
+    ctx = make_context(wl, inp, streamed=True)
+    for window, sinks in ((256, 0), (100, 4)):
+        ctx.set_attention_window(window, sinks)
+        loss, grads, _ = run_step(ctx, wl, inp, want_logits=False)
+        ref = M.step(wl, raw_layers=inp["raw"], head=inp["head"], tokens=inp["tokens"], targets=inp["targets"], bf16_acts=True,
+                     window=window, sinks=sinks)
+        assert abs(loss - ref["loss"]) <= LOSS_RTOL * abs(ref["loss"])
+        got = compare_grads(ctx, grads, ref["grads"])
+        print("window", window, "sinks", sinks, "worst:", sorted(got, key=lambda x: -x[4])[:3])
+        for l, p, w, cs, mr in got:
+            assert cs >= GRAD_COS and mr <= GRAD_MAXREL, (l, p, w, cs, mr)
+    ctx.close()
