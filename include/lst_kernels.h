@@ -161,6 +161,7 @@ lst_status lst_k_cross_entropy(const float* logits, int64_t T, int32_t V, const 
  *   logp_t = logits[t][y_t] - logsumexp(logits[t]),  r = exp(logp_t - old_logp[t]),
  *   u = min(r A, clip(r, 1 - clip_lo, 1 + clip_hi) A),
  *   kl = exp(ref_logp[t] - logp_t) - (ref_logp[t] - logp_t) - 1,  l_t = -u + kl_beta kl;
+ * where u_t = 0 if A = 0, and no KL term if kl_beta = 0, also where r or kl overflows;
  * out [4] = sums of w_t times l_t (the loss), kl, 1 where the clip lowered u else 0, and r;
  * logp [T] = logp_t (0 on tokens that do not count);
  * dlogits bf16 [T, V] (NULL: loss only) = w_t dl_t/dlogp_t (onehot(y_t) - softmax(logits[t])), with

@@ -59,17 +59,18 @@ __device__ __forceinline__ float k3_term(float d) {
     t = fmaf(t, d, 0.5f);
     return t * d * d;
   }
-  return expm1f(d) - d;
+  return d < INFINITY ? expm1f(d) - d : d;
 }
 
-// One token's terms (l, kl, clipped, r) and dl/dlogp.
+// One token's terms (l, kl, clipped, r) and dl/dlogp. Factors of zero take out what overflowed beside them: an
+// advantage of 0 the ratio, a weight of 0 the KL term.
 struct Token {
   float4 terms;
   float slope;
 };
 __device__ __forceinline__ Token policy_token(const PolicyArgs& a, float A, float old, float ref, float logp) {
   const float r = a.old_logp ? expf(logp - old) : 1.f;
-  const float in = r * A, cl = fminf(fmaxf(r, 1.f - a.lo), 1.f + a.hi) * A;
+  const float ra = A != 0.f ? r : 1.f, in = ra * A, cl = fminf(fmaxf(ra, 1.f - a.lo), 1.f + a.hi) * A;
   const bool cut = in > cl;  // the clip lowers the surrogate: no gradient
   float kl = 0.f, dkl = 0.f;
   if (a.ref_logp) {
@@ -77,7 +78,9 @@ __device__ __forceinline__ Token policy_token(const PolicyArgs& a, float A, floa
     kl = k3_term(d);
     dkl = -expm1f(d);
   }
-  return {make_float4(fmaf(a.beta, kl, -(cut ? cl : in)), kl, cut ? 1.f : 0.f, r), fmaf(a.beta, dkl, cut ? 0.f : -in)};
+  const bool on = a.beta != 0.f;
+  return {make_float4(fmaf(a.beta, on ? kl : 0.f, -(cut ? cl : in)), kl, cut ? 1.f : 0.f, r),
+          fmaf(a.beta, on ? dkl : 0.f, cut ? 0.f : -in)};
 }
 
 // One CTA: counts the mask and leaves the weight of a counted token of each sequence. What is counted:

@@ -10,7 +10,7 @@ namespace lst {
 // Per token t with mask_t != 0 (all when mask is null), logits row x_t, target y_t:
 //   logp = x[y] - lse(x);  r = exp(logp - old);  u = min(r A, clip(r, 1 - lo, 1 + hi) A);
 //   kl = exp(ref - logp) - (ref - logp) - 1;     l = -u + beta kl,
-// weighted by w_t of `norm` (0: m / sum m; 1: m / (nseq sum_seq m); 2: m / T).
+// (u = 0 where A = 0, no KL term where beta = 0, whatever overflows beside them), weighted by w_t of `norm` (0: m / sum m; 1: m / (nseq sum_seq m); 2: m / T).
 struct PolicyArgs {
   const float* logits;  // rows [row0, row0 + rows) of [T, V]
   int64_t T;

@@ -580,16 +580,20 @@ def policy_weights(mask, nseq, seq, norm):
 def policy_loss(logp, old, ref, adv, w, lo, hi, beta):
     """(out [4], d loss / d logp [T]) from per-token log-probabilities and advantages; old None:
     ratio 1; ref None: no KL term. out: sums of w times loss, kl, [clipped], ratio."""
-    r = np.exp(logp - old) if old is not None else np.ones_like(logp)
-    inner, outer = r * adv, np.clip(r, 1.0 - lo, 1.0 + hi) * adv
-    cut = inner > outer
-    d = ref - logp if ref is not None else np.zeros_like(logp)
-    kl = np.expm1(d) - d
-    token = -np.minimum(inner, outer) + beta * kl
-    slope = np.where(cut, 0.0, -inner) - beta * np.expm1(d)
     on = w > 0
-    out = np.array([np.sum((w * a)[on]) for a in (token, kl, cut.astype(F64), r)])
-    return out, np.where(on, w * slope, 0.0)
+    with np.errstate(over="ignore", invalid="ignore"):
+        r = np.exp(logp - old) if old is not None else np.ones_like(logp)
+        # factors of zero take out what overflowed beside them
+        inner = np.where(adv != 0, r * adv, 0.0)
+        outer = np.where(adv != 0, np.clip(r, 1.0 - lo, 1.0 + hi) * adv, 0.0)
+        cut = inner > outer
+        d = ref - logp if ref is not None else np.zeros_like(logp)
+        kl = np.where(d < np.inf, np.expm1(d) - d, d)
+        token, slope = -np.minimum(inner, outer), np.where(cut, 0.0, -inner)
+        if beta != 0:
+            token, slope = token + beta * kl, slope - beta * np.expm1(d)
+    out = np.array([np.sum(w[on] * a[on]) for a in (token, kl, cut.astype(F64), r)])
+    return out, np.where(on, w * np.where(on, slope, 0.0), 0.0)
 
 
 def policy_dlogits(logits, targets, old, ref, adv, mask, nseq, seq, norm, lo, hi, beta):

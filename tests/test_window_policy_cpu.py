@@ -182,3 +182,14 @@ def test_null_context_is_refused():
     assert L.lst_set_attention_window(None, 4, 0) == 1
     assert L.lst_get_logp(None, None) == 1
     assert L.lst_step_policy(None, None, None, None, None, None, 1, 1, None, None, None) == 1
+
+
+def test_policy_factors_of_zero_take_out_what_overflows():
+    # an advantage of 0 the ratio, a weight of 0 the KL term; one that counts stays infinite
+    logp, old, ref = np.array([-1.0, -1.0, -np.inf]), np.array([-1000.0, -1.2, -1.0]), np.array([-1.0, 1000.0, -1.0])
+    w, adv = np.full(3, 1 / 3), np.array([0.0, 2.0, -1.0])
+    out, g = M.policy_loss(logp, old, ref, adv, w, 0.2, 0.2, 0.0)
+    assert np.all(np.isfinite(out[[0, 2]])) and np.all(np.isinf(out[[1, 3]])) and np.all(np.isfinite(g))
+    assert g[0] == 0 and out[0] == pytest.approx((-1.2 * 2 + 0.8) / 3)
+    out, g = M.policy_loss(logp, old, ref, adv, w, 0.2, 0.2, 0.1)
+    assert np.isposinf(out[0]) and g[0] == 0 and np.isneginf(g[1])
