@@ -161,7 +161,7 @@ def _ptr(x) -> int | None:
     except AttributeError:
         return _other_ptr(x)
     # row-strided views are fine: every entry point takes explicit leading dimensions
-    if stride and stride[-1] != 1 and x.shape[-1] > 1:
+    if stride and stride[-1] != 1 and x.numel() > 1:
         raise ValueError("innermost dimension must be contiguous")
     return x.data_ptr()
 

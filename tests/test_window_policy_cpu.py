@@ -193,3 +193,13 @@ def test_policy_factors_of_zero_take_out_what_overflows():
     assert g[0] == 0 and out[0] == pytest.approx((-1.2 * 2 + 0.8) / 3)
     out, g = M.policy_loss(logp, old, ref, adv, w, 0.2, 0.2, 0.1)
     assert np.isposinf(out[0]) and g[0] == 0 and np.isneginf(g[1])
+
+
+def test_pointer_of_a_strided_column_is_refused():
+    # [4, 1] with an innermost stride of its own: no leading dimension tells an entry point about its rows
+    x = torch.arange(8.0)
+    for y in (x.as_strided((4, 1), (2, 3)), x.view(4, 2)[:, :1].t().as_strided((4, 1), (2, 2)), x.view(1, 8).t()):
+        with pytest.raises(ValueError):
+            lst._ptr(y)
+    assert lst._ptr(x.view(8, 1)) == x.data_ptr()  # contiguous
+    assert lst._ptr(x[:1].as_strided((1, 1), (5, 7))) == x.data_ptr()  # one element
