@@ -340,6 +340,7 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int 
             const int at = 4 * c - off + lane;
             if (lane < 4) buf[4 * (c - b) + lane] = at >= 0 && at < a.V ? x[at] : -INFINITY;
           }
+          if (!ALIGNED) fence_proxy_async();  // a later row's bulk copy writes where these stores have written
           __syncwarp();
           if (lane == 0) {
             if (hi > lo) {
