@@ -740,10 +740,11 @@ cudaError_t policy_rows(const PolicyArgs& a, int64_t row0, int64_t rows, bool ea
   // A warp takes up to 1024 slots, in registers for 4, 16 or 32 a lane (3344 rows of 500 logits 10 us, of 4000 21 us;
   // by clusters 29 and 27). A CTA of a cluster takes up to 4750 slots (224 consumers of 22, three half slices of
   // shared memory), two CTAs an SM. A few rows are spread further, so that every SM has some of them, and a
-  // shorter slice is a shorter chain for a row.
+  // shorter slice is a shorter chain for a row. All of it goes by the call's rows, not by this range's: the order in
+  // which a row's sum and the rows' terms are added follows from it, and is the same however the rows are cut.
   const int slots = (a.V + 6) / 4;
   int cs = 1;
-  while (cs < 8 && ((slots + cs - 1) / cs > 4750 || (rows * cs < 2 * device_sm_count() && slots / cs > 1024))) cs *= 2;
+  while (cs < 8 && ((slots + cs - 1) / cs > 4750 || (a.T * cs < 2 * device_sm_count() && slots / cs > 1024))) cs *= 2;
   const int slice = (slots + cs - 1) / cs;
   cudaError_t e;
   const auto warps = [&](auto kernel) {

@@ -33,7 +33,9 @@ constexpr int kPolicyMaxV = 1 << 20;
 bool policy_cfg_ok(float lo, float hi, float beta, int norm);
 bool policy_args_ok(const PolicyArgs& a);
 // The call is policy_begin, then policy_rows over ranges of rows that cover [0, T) once; the last row
-// to finish adds the row terms up in row order and writes out. The ranges may share one logits buffer.
+// to finish adds the terms of all rows up in a fixed order and writes out. The ranges may share one logits
+// buffer. The results have the same bytes whatever the ranges, as long as V is a multiple of 4 and every range's
+// logits lie alike in 16 bytes: a row's sum is added by its 16-byte slots.
 // early: policy_begin is the launch right in front on the stream, so that the rows' loads need not wait for it.
 cudaError_t policy_begin(const PolicyArgs& a, cudaStream_t s);
 cudaError_t policy_rows(const PolicyArgs& a, int64_t row0, int64_t rows, bool early, cudaStream_t s);
