@@ -339,8 +339,8 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int 
             if (c >= lo && c < hi) continue;
             const int at = 4 * c - off + lane;
             if (lane < 4) buf[4 * (c - b) + lane] = at >= 0 && at < a.V ? x[at] : -INFINITY;
+            if (!ALIGNED) fence_proxy_async();  // a later row's bulk copy writes where these stores have written
           }
-          if (!ALIGNED) fence_proxy_async();  // a later row's bulk copy writes where these stores have written
           __syncwarp();
           if (lane == 0) {
             if (hi > lo) {
@@ -707,12 +707,16 @@ cudaError_t launch_cluster_as(const PolicyArgs& a, int64_t row0, int64_t rows, i
                   rows, slice, early ? 1 : 0);
 }
 
-template <int NV, int THREADS, int PER_SM>
+// Every row starts and ends with a 16-byte slot.
+bool rows_aligned(const PolicyArgs& a) { return a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0; }
+
+// PER_SM, PER_SM_U: CTAs an SM where rows are aligned and where they are not.
+template <int NV, int THREADS, int PER_SM, int PER_SM_U = PER_SM>
 cudaError_t launch_cluster(const PolicyArgs& a, int64_t row0, int64_t rows, int cs, int slice, bool early,
                            cudaStream_t s) {
-  return a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0
+  return rows_aligned(a)
              ? launch_cluster_as<NV, THREADS, PER_SM, true>(a, row0, rows, cs, slice, early, s)
-             : launch_cluster_as<NV, THREADS, PER_SM, false>(a, row0, rows, cs, slice, early, s);
+             : launch_cluster_as<NV, THREADS, PER_SM_U, false>(a, row0, rows, cs, slice, early, s);
 }
 
 }  // namespace
@@ -746,6 +750,12 @@ cudaError_t policy_rows(const PolicyArgs& a, int64_t row0, int64_t rows, bool ea
   int cs = 1;
   while (cs < 8 && ((slots + cs - 1) / cs > 4750 || (a.T * cs < 2 * device_sm_count() && slots / cs > 1024))) cs *= 2;
   const int slice = (slots + cs - 1) / cs;
+  // Short slices are held by threads of 6 slots, four CTAs an SM, up to what those hold, 1536 (3000 rows of 4100 logits
+  // 20.7 us, of 6136 25.3, 48 rows of 9000 7.8; by threads of 22 slots 21.7, 25.5 and 8.5). Where rows are not aligned,
+  // whose code needs more registers, three an SM and only to 1152 (3000 rows of 4099 logits 22.1 us against 23.5, 48
+  // rows of 9001 7.9 against 8.8; with longer slices 3000 rows of 5003 took 26.1 against 24.1, of 6131 29.2 against 28.4;
+  // at four an SM, with spills, 25.2 and 29.0).
+  const int small = rows_aligned(a) ? 1536 : 1152;
   cudaError_t e;
   const auto warps = [&](auto kernel) {
     return launch_k(kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, 0, a, row0, rows, early ? 1 : 0);
@@ -753,7 +763,7 @@ cudaError_t policy_rows(const PolicyArgs& a, int64_t row0, int64_t rows, bool ea
   if (slots <= 32 * 4) e = warps(k_policy_warp<4>);
   else if (slots <= 32 * 16) e = warps(k_policy_warp<16>);
   else if (slots <= 32 * 32) e = warps(k_policy_warp<32>);
-  else if (slice <= 1536) e = launch_cluster<6, 288, 4>(a, row0, rows, cs, slice, early, s);
+  else if (slice <= small) e = launch_cluster<6, 288, 4, 3>(a, row0, rows, cs, slice, early, s);
   else if (slice <= 4750) e = launch_cluster<22, 256, 2>(a, row0, rows, cs, slice, early, s);
   else if (slice <= 9400) e = launch_cluster<22, 512, 1>(a, row0, rows, cs, slice, early, s);
   else e = launch_k(k_policy_rows, dim3((unsigned)rows), dim3(512), 0, s, 0, a, row0);
