@@ -913,7 +913,8 @@ k_window_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUt
 // CTA instead, 685 MB came from HBM for 9472 tokens rather than 196, and the kernel took 10 % longer); the rest
 // is cut, at fixed places, to make the CTAs' work equal. What a tile costs besides its items (K, V, the
 // stores) counts as kSeg items in front of them, which also moves cuts next to a tile's border onto the
-// border. The sums of a cut tile's parts go to the scratch as fp32, where k_window_join adds them in order.
+// border (with 1 item 2048 tokens, 32 heads of 128 over 8, window 512 take 85.4 us instead of 81.0, 1024 tokens, window
+// 1024, 47.6 instead of 45.8; with 4 items 81.3 and 46.2, and 2 x 512, window 256, 37.8 instead of 37.1). The sums of a cut tile's parts go to the scratch as fp32, where k_window_join adds them in order.
 constexpr int kSms = 148, kSeg = 2;
 struct Split {
   int nkb, nsb;  // key tiles of a sequence, those that hold sinks
@@ -1292,8 +1293,9 @@ __global__ void __launch_bounds__(256) k_window_join(const WinBwdArgs p, const _
 
 // How the dK / dV work is dealt out. As many rounds of whole tiles as leave no CTA with more than its share; where
 // the tiles are as few as the SMs, a CTA each, if the longest of them takes no longer than equal shares and the
-// stores and the kernel that join them (about kJoin items: the backward of 4 sequences of 512 tokens took 65 us in
-// whole tiles of up to 16 items, 69 us in shares of 8.6).
+// stores and the kernel that join them (about kJoin items). Backward in whole tiles and in shares, by how many items the
+// longest tile is above an equal share: 4, 8 x 256 tokens, 36 us against 45; 8, 4 x 512, 52.5 against 57.0; 9, 2048
+// tokens, 8 heads each of its own, 51.1 against 53.3; 12, 300 tokens, 30.5 against 27.5; 13, 2 x 512, 42.5 against 37.0.
 constexpr int kJoin = 10;
 Split make_split(int64_t T, int S, int hq, int hkv, int window, int sinks) {
   const int64_t units = T / S * hkv;
