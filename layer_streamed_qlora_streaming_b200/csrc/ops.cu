@@ -5,6 +5,7 @@
 // partials summed in index order), so results do not depend on scheduling: the streamed and the
 // resident schedule run the same launches and give the same bytes.
 #include "common.cuh"
+#include "sync.cuh"
 #include "pdl.cuh"
 #include "ex2.cuh"
 #include "ops.cuh"
@@ -336,12 +337,6 @@ k_ce(const float* __restrict__ logits, int V, const int32_t* __restrict__ y, flo
 // (the SFU's approximate exp2 on the product, formed with one fma). Needs V % 4 == 0 (16-byte
 // aligned slices).
 constexpr int kCeThreads = 256, kCeChunks = 4;
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 // block-wide max / sum of one value per thread (kCeThreads), fixed tree; every thread gets it
 __device__ __forceinline__ float ce_block_max(float v, float* red) {
 #pragma unroll

@@ -5,6 +5,7 @@
 // Each logit crosses HBM once: a warp (k_policy_warp) or a cluster of CTAs (k_policy_cluster) holds a row in
 // registers from its load to the store of dlogits; only rows too long for that are read twice (k_policy_rows).
 #include "common.cuh"
+#include "sync.cuh"
 #include "pdl.cuh"
 #include "ex2.cuh"
 #include "policy.cuh"
@@ -17,12 +18,6 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ void bulk_store(uintptr_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"((uint64_t)dst), "r"(smem_u32(src)),
                "r"(bytes)
@@ -152,19 +147,6 @@ __device__ __forceinline__ float lane_sum(float x) {
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-__device__ __forceinline__ bool named_all(int id, int threads, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "barrier.red.and.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"((uint32_t)ok)
-      : "memory");
-  return r != 0;
 }
 
 // Once thread 0 has stored the terms of its `done` rows: the last CTA of the call to get here adds the
@@ -453,7 +435,7 @@ k_policy_cluster(const PolicyArgs a, int64_t row0, int64_t rows, int slice, int 
         }
       }
     }
-    ok = named_all(1, nc, ok);  // a lost pair ends the loop for every consumer
+    ok = sync_all(1, nc, ok);  // a lost pair ends the loop for every consumer
     if (!d) continue;
     const float lse2 = factor.x, coef = factor.y, f = coef * ex2_approx(m - lse2);
     const auto packed = [&](int n) {

@@ -15,6 +15,7 @@
 // backward's P rounded (half a step of 2^-8 relative each, independent of the output's own rounding), the
 // forward's P rounded too or held in two bf16 parts (WinArgs::parts). Scores, lse, sums and products are fp32.
 #include "common.cuh"
+#include "sync.cuh"
 #include "pdl.cuh"
 #include "ex2.cuh"
 #include "gemm.cuh"
@@ -121,26 +122,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 
-// Barrier of `threads` threads (whole warps); true for all of them when ok holds for all.
-__device__ __forceinline__ bool sync_all(int id, int threads, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "barrier.red.and.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"((uint32_t)ok)
-      : "memory");
-  return r != 0;
-}
 // Wait of a whole warp; false (for all of it) once it ran out. Not unrolled: there are many of them, and the
 // kernels' code has to stay in the instruction cache (dQ with 111 KB of code took 3000 clocks a block).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
