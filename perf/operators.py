@@ -245,7 +245,7 @@ def run(state):
             state["scratch"] = torch.empty(lst.attention_window_scratch(T, c["S"], hq, hkv, hd, c["window"], c["sinks"]),
                                            device="cuda")
         lst.k_attention_window_bwd(state["q"], ld, state["k"], ld, state["v"], ld, state["o"], hq * hd, state["dout"],
-                                   hq * hd, state["lse"], state["scratch"], state["dq"], ld, state["dk"], ld, state["dv"],
+                                   hq * hd, state["lse"].contiguous(), state["scratch"], state["dq"], ld, state["dk"], ld, state["dv"],
                                    ld, T, c["S"], hq, hkv, hd, c["window"], c["sinks"], stream=s)
         return state["dq"], state["dk"], state["dv"]
     return {"fwd": _forward, "bwd": _backward, "policy": _loss}[c["op"]](state)
