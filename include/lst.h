@@ -221,8 +221,8 @@ typedef struct {
  * do not count are not read for values. out: HOST float [4] = loss, mean KL estimate, share of clipped
  * tokens, mean ratio, each weighted as cfg->norm says; grads as in lst_step. With kl_beta > 0 the step
  * starts with the reference forward (3L layer reads instead of 2L, or fewer with reuse). The first call
- * allocates the step's buffers (6 * max_batch * max_seq fp32 and a few). Needs vocab > 0,
- * n_seq <= max_batch, seq <= max_seq. */
+ * allocates the step's buffers (9 * max_batch * max_seq fp32 and a few). Means are over this call's tokens.
+ * The results have the same bytes with any head_chunk. Needs vocab > 0, n_seq <= max_batch, seq <= max_seq. */
 lst_status lst_step_policy(lst_ctx* ctx, const int32_t* tokens, const int32_t* targets,
                            const int32_t* mask, const float* old_logp, const float* adv, int32_t n_seq,
                            int32_t seq, const lst_policy* cfg, float* out, float* grads);
@@ -232,9 +232,13 @@ lst_status lst_step_policy(lst_ctx* ctx, const int32_t* tokens, const int32_t* t
  * samples. LST_ERR_STATE unless the last step was lst_step_policy. */
 lst_status lst_get_logp(lst_ctx* ctx, float* dst);
 
-/* Attention of the next steps: query i sees key j <= i of its sequence when i - j < window or
- * j < sinks. window 0 (default): plain causal attention. The backward's scratch is allocated by the
- * first step that needs more of it. LST_ERR_ARG for negative values. */
+/* Attention of the next steps, in every layer: query i sees key j <= i of its sequence when i - j < window
+ * or j < sinks. window 0 (default): plain causal attention. Positions stay those of the whole sequence: a
+ * sampler whose cache of sinks and window numbers its entries anew at every token rotates its keys otherwise,
+ * and its log-probabilities are not this step's. The probabilities enter P V with 16 bits and the backward
+ * reads the unrounded output, so that a window costs a step no bits. The backward's scratch is allocated by
+ * the first step that needs more of it. LST_ERR_ARG for negative values, and for sizes of max_batch, max_seq
+ * that lst_k_attention_window_fwd refuses. */
 lst_status lst_set_attention_window(lst_ctx* ctx, int32_t window, int32_t sinks);
 
 /* Copy the last step's logits [batch * seq, V] fp32 to dst (host or device). */

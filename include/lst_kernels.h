@@ -105,9 +105,10 @@ lst_status lst_k_attention_bwd(const uint16_t* q, int64_t ldq, const uint16_t* k
  * are sampled this way, with a cache of the last `window` tokens and the first `sinks` ones; training
  * on them has to see the same keys. Arguments as lst_k_attention_fwd (any hq a multiple of hkv), o
  * 16-byte aligned with ldo a multiple of 8; window >= 1, sinks >= 0; S at most 2^30, T * hq below
- * 2^31, T / S * hkv below 2^16. The probabilities enter the P V product as bf16, so v has bf16's
- * range. Rows of one sequence never
- * reach another's result; within a sequence a NaN or infinity in k or v may reach queries that share
+ * 2^31, T / S * hkv below 2^16. The probabilities enter the P V product as bf16 (8 bits, where
+ * lst_k_attention_fwd keeps 11 and limits v to fp16's range; a step of lst.h keeps 16). The sampler must keep
+ * the positions of the whole sequence in its rotary embedding; its keys are not these otherwise. Rows of one
+ * sequence never reach another's result; within a sequence a NaN or infinity in k or v may reach queries that share
  * a 128-row tile with its visible ones. No output overlaps an input. */
 lst_status lst_k_attention_window_fwd(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk,
                                       const uint16_t* v, int64_t ldv, uint16_t* o, int64_t ldo,
@@ -115,8 +116,10 @@ lst_status lst_k_attention_window_fwd(const uint16_t* q, int64_t ldq, const uint
                                       int32_t hd, int32_t window, int32_t sinks, void* stream);
 
 /* Its backward: dq, dk, dv bf16 (16-byte aligned, row strides multiples of 8) from dout and the
- * forward's o and lse; dk and dv add the query heads of their group. scratch: fp32
- * [lst_k_attention_window_scratch(...)], 16-byte aligned, not shared by calls that may overlap on the
+ * forward's o and lse; dk and dv add the query heads of their group. D = dout . o is formed from the
+ * bf16 o: dq carries its rounding, dout . (exact o - o), times the mean of the keys that a row sees, which
+ * is far from small where keys and values share an offset (as in lst_k_attention_bwd; a step of lst.h uses the
+ * unrounded o). scratch: fp32 [lst_k_attention_window_scratch(...)], 16-byte aligned, not shared by calls that may overlap on the
  * GPU. No output overlaps an input or the scratch. Deterministic (no atomics). */
 lst_status lst_k_attention_window_bwd(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk,
                                       const uint16_t* v, int64_t ldv, const uint16_t* o, int64_t ldo,
