@@ -211,7 +211,7 @@ constexpr int kZeroBytes = 1024;
 //    (st.async of each CTA's pair into its peers, onto their mbarrier), in a fixed order; the row's
 //    factor coef 2^((m - lse) log2 e) then turns e into dlogits with one product.
 // Each logit crosses HBM once and takes one exponential. Bound by HBM: 4 + 2 bytes a logit, 2 bytes on rows that
-// do not count: 4096 rows of 151936 logits, most of them counted, take 442 to 458 us by the box, 0.92 to 0.95 of the
+// do not count: 4096 rows of 151936 logits, most of them counted, take 442 to 458 us from card to card, 0.92 to 0.95 of the
 // rate of a plain copy; 2048 rows of 128256 250 us (0.97), with half of them counted 179 us (0.90); 999 rows of 32003, of which
 // less than half count, 25 us (0.57): a few rows a cluster, each a chain of load, exchange and stores.
 // (A CTA a row, read twice: 3896 us for the first, 1461 for the half counted, 75 for the last. The slots of a thread

@@ -129,6 +129,7 @@ class Many:
 
 @pytest.mark.parametrize("T,V,S,offset", [
     (1500, 4100, 100, 0), (1500, 4099, 100, 1),     # several short rows a CTA
+    (1500, 5000, 100, 0), (1500, 5003, 100, 1),     # either side of the bound of short slices
     (1500, 16384, 50, 0), (1500, 16383, 50, 2),     # several long ones
     (400, 32000, 100, 0), (400, 32003, 100, 0),     # clusters of two, whose rows start anywhere in 16 bytes
     (200, 128256, 40, 0),                           # of eight

@@ -146,14 +146,11 @@ def test_32b_shaped_layers_under_a_window():
     wl = syn.WORKLOADS["qwen32b"].with_(n_layers=2, batch=1, seq=256)
     inp = build_inputs(wl)
     ctx = make_context(wl, inp, streamed=True)
-    for window, sinks in ((256, 0), (100, 4)):
-        ctx.set_attention_window(window, sinks)
-        loss, grads, _ = run_step(ctx, wl, inp, want_logits=False)
-        ref = M.step(wl, raw_layers=inp["raw"], head=inp["head"], tokens=inp["tokens"], targets=inp["targets"], bf16_acts=True,
-                     window=window, sinks=sinks)
-        assert abs(loss - ref["loss"]) <= LOSS_RTOL * abs(ref["loss"])
-        got = compare_grads(ctx, grads, ref["grads"])
-        print("window", window, "sinks", sinks, "worst:", sorted(got, key=lambda x: -x[4])[:3])
-        for l, p, w, cs, mr in got:
-            assert cs >= GRAD_COS and mr <= GRAD_MAXREL, (l, p, w, cs, mr)
+    window, sinks = 100, 4
+    ctx.set_attention_window(window, sinks)
+    loss, grads, _ = run_step(ctx, wl, inp, want_logits=False)
     ctx.close()
+    ref = M.step(wl, raw_layers=inp["raw"], head=inp["head"], tokens=inp["tokens"], targets=inp["targets"], bf16_acts=True,
+                 window=window, sinks=sinks)
+    assert abs(loss - ref["loss"]) <= LOSS_RTOL * abs(ref["loss"])
+    _check_grads(ctx, grads, ref["grads"])
